@@ -2,8 +2,9 @@
 MI355X, with the n rank buffers resident in its HBM.
 
 This package is a thin ctypes binding over ``libar.so`` (HIP kernels for
-gfx950 plus the C ABI declared in ``include/ar.h`` and, for the M-to-N layout
-reshard, ``include/ar_reshard.h``).  The functions keep the C
+gfx950 plus the C ABI declared in ``include/ar.h``, for the M-to-N layout
+reshard ``include/ar_reshard.h`` and for the reductions over a vocabulary axis
+split over the ranks ``include/ar_vocab.h``).  The functions keep the C
 names and only marshal arguments: every step of the collective runs in the
 library's kernels.  There is no CPU fallback; importing the package fails
 loudly when the library has not been built (``python
@@ -39,6 +40,15 @@ from ._binding import (  # noqa: F401
     ar_reshard,
     ar_reshard_plan,
     local_shape,
+    VocabShape,
+    vocab_widths,
+    ar_vocab_workspace,
+    ar_logprobs,
+    ar_logprobs_backward,
+    ar_logprobs_grad,
+    ar_distill,
+    ar_distill_backward,
+    ar_distill_grad,
 )
 
 __all__ = [
@@ -69,4 +79,13 @@ __all__ = [
     "ar_reshard",
     "ar_reshard_plan",
     "local_shape",
+    "VocabShape",
+    "vocab_widths",
+    "ar_vocab_workspace",
+    "ar_logprobs",
+    "ar_logprobs_backward",
+    "ar_logprobs_grad",
+    "ar_distill",
+    "ar_distill_backward",
+    "ar_distill_grad",
 ]

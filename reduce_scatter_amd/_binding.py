@@ -131,6 +131,7 @@ class PointerTable:
 
     def __init__(self, bufs):
         self.n = len(bufs)
+        self._checked = None             # the last shape these buffers were checked against
         self.array = (ctypes.c_void_p * max(1, self.n))(*[_ptr(b) for b in bufs])
         self._bufs = list(bufs)          # tensors stay alive (and their memory owned) while the table exists
 
@@ -371,3 +372,174 @@ def ar_reshard(src_bufs, dst_bufs, src, dst, elem_size, route="auto", stream=Non
     ls, ld = _layout(src), _layout(dst)
     _check(_lib.ar_reshard(_ptr_array(src_bufs), _ptr_array(dst_bufs), ctypes.byref(ls), ctypes.byref(ld),
                            elem_size, _code(ROUTES, route, "route"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Reductions over a vocabulary axis split over the ranks (include/ar_vocab.h)
+# ---------------------------------------------------------------------------
+
+class _VocabStruct(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("dtype", ctypes.c_int), ("rows", ctypes.c_longlong),
+                ("widths", ctypes.POINTER(ctypes.c_longlong)), ("pitches", ctypes.POINTER(ctypes.c_longlong)),
+                ("grad_pitches", ctypes.POINTER(ctypes.c_longlong)), ("temperature", ctypes.c_float)]
+
+
+_vshape, _vp, _int = ctypes.POINTER(_VocabStruct), ctypes.c_void_p, ctypes.c_int
+_lib.ar_vocab_workspace.argtypes = [_vshape, _int, ctypes.POINTER(ctypes.c_size_t)]
+_lib.ar_logprobs.argtypes = [_vpp, _vshape, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.ar_logprobs_backward.argtypes = [_vpp, _vpp, _vshape, _vp, _vp, _vp, _vp, _vp]
+_lib.ar_logprobs_grad.argtypes = [_vpp, _vpp, _vshape, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.ar_distill.argtypes = [_vpp, _vshape, _vp, _vp, _int, _int, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.ar_distill_backward.argtypes = [_vpp, _vpp, _vshape, _vp, _vp, _int, _int, _vp, _vp, _vp]
+_lib.ar_distill_grad.argtypes = [_vpp, _vpp, _vshape, _vp, _vp, _int, _int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+for _f in (_lib.ar_vocab_workspace, _lib.ar_logprobs, _lib.ar_logprobs_backward, _lib.ar_logprobs_grad,
+           _lib.ar_distill, _lib.ar_distill_backward, _lib.ar_distill_grad):
+    _f.restype = ctypes.c_int
+
+
+class VocabShape:
+    """Rows of logits whose vocabulary axis lies in n rank buffers: rank r
+    holds ``widths[r]`` columns of every row, rows ``pitches[r]`` elements
+    apart (default: the widths), gradients ``grad_pitches[r]`` (default: the
+    pitches).  Built once and reusable across calls."""
+
+    def __init__(self, rows, widths, dtype, pitches=None, grad_pitches=None, temperature=1.0):
+        self.rows, self.widths, self.n = int(rows), [int(w) for w in widths], len(widths)
+        for p in (pitches, grad_pitches):
+            if p is not None and len(p) != self.n:
+                raise ValueError("one pitch per rank")
+        self.pitches = self.widths if pitches is None else [int(p) for p in pitches]
+        self.grad_pitches = self.pitches if grad_pitches is None else [int(p) for p in grad_pitches]
+        self.dtype, self.temperature = _dtype_code(dtype), float(temperature)
+        self._arrays = [(ctypes.c_longlong * max(1, self.n))(*a)
+                        for a in (self.widths, self.pitches, self.grad_pitches)]
+        self._struct = _VocabStruct(self.n, self.dtype, self.rows, *self._arrays, self.temperature)
+        self.ref = ctypes.byref(self._struct)
+
+
+def vocab_widths(vocab, n):
+    """Columns of each of n ranks under the shard bounds of ``ar_layout_shard``."""
+    return [(r + 1) * vocab // n - r * vocab // n for r in range(n)]
+
+
+def _logit_table(bufs, shape, grads=False):
+    """Pointer table of rank buffers; tensors must have the shape's type and hold its rows."""
+    if not isinstance(bufs, PointerTable):
+        bufs = PointerTable(bufs)
+    if bufs._checked != (shape, grads):
+        if bufs.n != shape.n:
+            raise ValueError("%d rank buffers for %d ranks" % (bufs.n, shape.n))
+        for b, w, p in zip(bufs._bufs, shape.widths, shape.grad_pitches if grads else shape.pitches):
+            if b is None or isinstance(b, int):
+                continue
+            if _dtype_code(b.dtype) != shape.dtype:
+                raise ValueError("rank buffer of %s does not have the shape's dtype" % b.dtype)
+            room = b.untyped_storage().nbytes() // b.element_size() - b.storage_offset()
+            if shape.rows and w and room < (shape.rows - 1) * p + w:
+                raise ValueError("rank buffer holds %d elements; %d rows of %d at pitch %d need more"
+                                 % (room, shape.rows, w, p))
+            if b.dim() == 2 and b.shape[0] > 1 and b.shape[1] > 0 and (b.stride(1) != 1 and b.shape[1] > 1
+                                                                       or b.stride(0) != p and shape.rows > 1):
+                raise ValueError("rank buffer has strides %s; its pitch is %d" % (tuple(b.stride()), p))
+        bufs._checked = (shape, grads)
+    return bufs.array
+
+
+def _vector(t, dtype, numel, what):
+    """Address of a contiguous tensor argument (integer addresses and None pass through)."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) != dtype or t.numel() < numel or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of at least %d elements" % (what, dtype, numel))
+    return t.data_ptr()
+
+
+def _f32(t, numel, what):
+    return _vector(t, "torch.float32", numel, what)
+
+
+def _i64(t, numel, what):
+    return _vector(t, "torch.int64", numel, what)
+
+
+def _workspace(w):
+    if w is None:
+        return None, 0
+    return w.data_ptr() or None, w.numel() * w.element_size()
+
+
+def ar_vocab_workspace(shape, top_k=0) -> int:
+    """Workspace bytes of the calls below on ``shape`` (host only)."""
+    n = ctypes.c_size_t()
+    _check(_lib.ar_vocab_workspace(shape.ref, top_k, ctypes.byref(n)))
+    return n.value
+
+
+def ar_logprobs(logits, shape, targets, logprobs, entropy=None, top_k=0, top_logprobs=None, top_ids=None, saved=None,
+                workspace=None, stream=None):
+    """ln p of each row's target; optionally the entropy, the ``top_k`` most
+    likely entries, and the statistics ``ar_logprobs_backward`` needs."""
+    r, (ws, wb) = shape.rows, _workspace(workspace)
+    _check(_lib.ar_logprobs(_logit_table(logits, shape), shape.ref, _i64(targets, r, "targets"),
+                            _f32(logprobs, r, "logprobs"), _f32(entropy, r, "entropy"), top_k,
+                            _f32(top_logprobs, r * top_k, "top_logprobs"), _i64(top_ids, r * top_k, "top_ids"),
+                            _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+
+
+def ar_logprobs_backward(logits, grads, shape, targets, saved, grad_logprobs=None, grad_entropy=None, stream=None):
+    """Gradient of the logits from the gradients of the log probabilities and entropies."""
+    r = shape.rows
+    _check(_lib.ar_logprobs_backward(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref,
+                                     _i64(targets, r, "targets"), _f32(saved, 4 * r, "saved"),
+                                     _f32(grad_logprobs, r, "grad_logprobs"), _f32(grad_entropy, r, "grad_entropy"),
+                                     _stream(stream)))
+
+
+def ar_logprobs_grad(logits, grads, shape, targets, logprobs=None, grad_logprobs=None, grad_entropy=None,
+                     entropy=None, saved=None, workspace=None, stream=None):
+    """Log probabilities (optionally entropies) and the gradient in one call."""
+    r, (ws, wb) = shape.rows, _workspace(workspace)
+    _check(_lib.ar_logprobs_grad(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref,
+                                 _i64(targets, r, "targets"), _f32(grad_logprobs, r, "grad_logprobs"),
+                                 _f32(grad_entropy, r, "grad_entropy"), _f32(logprobs, r, "logprobs"),
+                                 _f32(entropy, r, "entropy"), _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+
+
+def _teacher(shape, ids, values, k):
+    """(k, ids address, values address): k from a two-dimensional list of ids unless given."""
+    if k is None:
+        if ids is None or isinstance(ids, int) or ids.dim() != 2:
+            raise ValueError("k is needed unless teacher_ids is a two-dimensional tensor")
+        k = ids.shape[1]
+    return k, _i64(ids, shape.rows * k, "teacher_ids"), _f32(values, shape.rows * k, "teacher_values")
+
+
+def ar_distill(logits, shape, teacher_ids, teacher_values, loss, tail=False, k=None, saved=None, workspace=None,
+               stream=None):
+    """Divergence of the student's distribution from a teacher's top entries
+    (``tail``: log probabilities with the remaining mass compared as well;
+    otherwise renormalised logits)."""
+    r, (ws, wb) = shape.rows, _workspace(workspace)
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
+    _check(_lib.ar_distill(_logit_table(logits, shape), shape.ref, ids, values, k, int(bool(tail)),
+                           _f32(loss, r, "loss"), _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+
+
+def ar_distill_backward(logits, grads, shape, teacher_ids, teacher_values, saved, tail=False, k=None, grad_loss=None,
+                        stream=None):
+    """Gradient of the logits from the gradients of the rows' losses (None: ones)."""
+    r = shape.rows
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
+    _check(_lib.ar_distill_backward(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref, ids,
+                                    values, k, int(bool(tail)), _f32(saved, 4 * r, "saved"),
+                                    _f32(grad_loss, r, "grad_loss"), _stream(stream)))
+
+
+def ar_distill_grad(logits, grads, shape, teacher_ids, teacher_values, loss=None, tail=False, k=None, grad_loss=None,
+                    saved=None, workspace=None, stream=None):
+    """The rows' losses and the gradient in one call."""
+    r, (ws, wb) = shape.rows, _workspace(workspace)
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
+    _check(_lib.ar_distill_grad(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref, ids, values,
+                                k, int(bool(tail)), _f32(grad_loss, r, "grad_loss"), _f32(loss, r, "loss"),
+                                _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))

@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libar.so")
 SOURCES = ["tree.hip", "tree_stream.hip", "tree_reg.hip", "fused.hip", "fused_rs.hip", "ring.hip", "split.hip", "fused_phase.hip", "elem.hip", "reshard.hip",
-           "api.cpp", "plan.cpp", "reshard_api.cpp"]
+           "logprobs.hip", "distill.hip", "api.cpp", "plan.cpp", "reshard_api.cpp", "vocab_api.cpp"]
 
 ARCH = "gfx950"
 # -ffp-contract=off: a multiply followed by an add (the avg pre-scale, then

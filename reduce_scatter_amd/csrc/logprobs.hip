@@ -1,0 +1,288 @@
+// logprobs.hip -- log probabilities of given tokens with entropy and top
+// alternatives over vocabulary-split rows, and their gradient.
+//
+// One pass over the logits: every lane keeps the sums of 2^t and t*2^t of its
+// vectors relative to a running reference (vocab_device.hpp) and, for the top
+// alternatives, its largest logit with the vector it stands in.  That costs
+// the stream nothing more, and it is enough: the k largest logits of a row
+// lie in the k lanes whose best logits come first in the (value, column)
+// order, so after the pass the best-of-lane keys are sorted, and only those k
+// lanes' vectors (k / (64 W) of the row) are read again and sorted.  The work
+// is bounded whatever the order of the logits.
+#include "dispatch.hpp"
+#include "vocab_device.hpp"
+#include "vocab_launch.hpp"
+
+namespace ar {
+
+// The statistics and results of a row once its sums are whole.
+struct RowResult {
+    float lse;                         // ln of the sum relative to the reference
+    float entropy;
+    bool empty;                        // no distribution: every logit -inf
+};
+__device__ __forceinline__ RowResult row_result(const Stats &st) {
+    RowResult r;
+    r.empty = st.m == kNegInf && st.s == 0.0f;
+    r.lse = logf(st.s);
+    const float h = r.lse - kLn2 * (st.s1 / st.s);
+    r.entropy = r.empty || h < 0.0f ? 0.0f : h;
+    return r;
+}
+
+template <int NR>
+__device__ __forceinline__ void write_row(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row, const Stats &st,
+                                          const RowResult &res, float xt, bool token) {
+    const Ref ref = make_ref(st.m, g.c);
+    if (a.logprobs) a.logprobs[row] = !token ? 0.0f : res.empty ? kNegInf : rel_ln(xt, ref, g.c, g.inv_t) - res.lse;
+    if (a.entropy) a.entropy[row] = res.entropy;
+    if (a.saved) {
+        float *o = a.saved + row * 4;
+        o[0] = st.m;
+        o[1] = st.s;
+        o[2] = res.entropy;
+        o[3] = 0.0f;
+    }
+}
+
+template <int NR>
+__device__ __forceinline__ void write_top(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row, const Stats &st,
+                                          const RowResult &res, u64 key, int lane) {
+    if (lane >= a.k) return;
+    const Ref ref = make_ref(st.m, g.c);
+    const float x = order_value((uint32_t)(key >> 32));
+    a.top_ids[row * a.k + lane] = key ? (int64_t)key_col(key) : -1;
+    a.top_logprobs[row * a.k + lane] = !key || res.empty ? kNegInf : rel_ln(x, ref, g.c, g.inv_t) - res.lse;
+}
+
+// The 64 largest keys of this workgroup's part of the row, of which the first
+// k are exact; best / col: each lane's largest logit and the first column of
+// its vector (col < 0: none).
+template <int DT, int NR>
+__device__ __forceinline__ u64 select_top(const VocabGeom<NR> &g, long long row, float best, int col, int k, u64 *lds,
+                                          int waves, int wave, int lane) {
+    constexpr int K = Lanes<DT>::value;
+    const int step = waves * g.parts;
+    const u64 list = block_lists(sort_down(col >= 0 ? top_key(best, col) : 0, lane), lds, waves, wave, lane);
+    const uint32_t floor = (uint32_t)(__shfl(list, k - 1) >> 32);      // no k-th largest logit is below it
+    u64 mine = 0;
+    for (int j = wave; j < k; j += waves) {
+        const u64 key = __shfl(list, j);
+        if (!key) break;
+        const Place p = place_of<DT>(g, key_col(key));
+        const int u = lane / K;                                        // lanes 0 .. U*K - 1 take one logit each
+        TileWalk t{0, __builtin_amdgcn_readfirstlane(p.t % step)};
+        for (t.settle<DT>(g); t.s < g.n; t.j += step, t.settle<DT>(g)) {
+            const int e = elem0<DT>(t.j, u, p.lane) + lane % K;
+            u64 cand = 0;
+            if (u < kVocabU && e < width_of<DT>(g, t.s)) {
+                const u64 c = top_key(load1<DT>(row_of<DT>(g, t.s, row), e), g.col0[t.s] + e);
+                if ((uint32_t)(c >> 32) >= floor) cand = c;
+            }
+            if (__any(cand != 0)) mine = merge_lists(mine, reversed(sort_down(cand, lane), lane), lane);
+        }
+    }
+    return block_lists(mine, lds, waves, wave, lane);
+}
+
+// Gradient of this workgroup's tiles: with e = 2^t and p = e / S,
+//   dx = [v = target] gl/T + e * (a0 + a1 t),
+//   a0 = -(gl + gh (H - ln S)) / (T S),  a1 = -gh ln2 / (T S).
+template <int DT, int NR>
+__device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row,
+                                               const Stats &st, const RowResult &res, int target, int first, int step,
+                                               int lane) {
+    constexpr int K = Lanes<DT>::value;
+    const float gl = a.grad_logprobs && target >= 0 ? a.grad_logprobs[row] : 0.0f;
+    const float gh = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
+    const bool zero = res.empty || (gl == 0.0f && gh == 0.0f);
+    const float a0 = -(gl + gh * (res.entropy - res.lse)) * g.inv_t / st.s;
+    const float a1 = -gh * kLn2 * g.inv_t / st.s;
+    const Ref ref = make_ref(st.m, g.c);
+    const Place p = target >= 0 ? place_of<DT>(g, target) : Place{-1, 0, 0, 0};
+    TileWalk t{0, first};
+    int at = first;
+    for (t.settle<DT>(g); t.s < g.n; t.j += step, at += step, t.settle<DT>(g)) {
+        const int w = width_of<DT>(g, t.s);
+        char *out = grad_row_of<DT>(g, t.s, row);
+        Tile<DT> x;
+        if (zero) {
+#pragma unroll
+            for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                for (int i = 0; i < K; ++i) x.v[u].v[i] = 0.0f;
+        } else {
+            load_tile<DT>(x, row_of<DT>(g, t.s, row), t.j, w, lane);
+            if (ref.wide) {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) x.v[u].v[i] = rel(x.v[u].v[i], ref, g.c);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) x.v[u].v[i] = __builtin_fmaf(x.v[u].v[i], g.c, -ref.y);
+            }
+            if (gh == 0.0f) {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) x.v[u].v[i] = exp2_fast(x.v[u].v[i]) * a0;
+            } else {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        const float tt = x.v[u].v[i];
+                        x.v[u].v[i] = exp2_fast(tt) * __builtin_fmaf(__builtin_fmaxf(tt, kTLow), a1, a0);
+                    }
+            }
+            if (at == p.t && lane == p.lane) {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u)
+#pragma unroll
+                    for (int i = 0; i < K; ++i)
+                        if (u == p.u && i == p.i) x.v[u].v[i] += gl * g.inv_t;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kVocabU; ++u) store_vec<DT>(out, x.v[u], elem0<DT>(t.j, u, lane), w);
+    }
+}
+
+__device__ __forceinline__ int token_of(const LogprobsArgs &a, long long row, int vocab) {
+    const int64_t t = a.targets[row];
+    return t >= 0 && t < vocab ? (int)t : -1;
+}
+
+// Statistics of a row (or of one part of it), the results where the row is
+// whole, and with BOTH its gradient by the same workgroup, which finds the
+// row's logits in the caches.
+template <int DT, int NR, bool S1, bool TOP, bool BOTH>
+__global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
+    __shared__ Stats lds_stats[kVocabWaves];
+    __shared__ u64 lds_keys[TOP ? kVocabWaves * 64 : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int waves = blockDim.x >> 6, step = waves * g.parts;
+    const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
+    const long long row = g.row0 + local;
+    const int first = part * waves + wave;
+    const int target = token_of(a, row, g.col0[g.n]);
+    const float xt = target >= 0 && g.parts == 1 ? logit_at<DT>(g, row, target) : 0.0f;
+
+    Stats st{kNegInf, 0.0f, 0.0f};
+    Ref ref = make_ref(kNegInf, g.c);
+    float limit = kNegInf, best = kNegInf;
+    int best_col = -1;
+    TileWalk t{0, first};
+    for (t.settle<DT>(g); t.s < g.n; t.j += step, t.settle<DT>(g)) {
+        const int w = width_of<DT>(g, t.s);
+        Tile<DT> x;
+        load_tile<DT>(x, row_of<DT>(g, t.s, row), t.j, w, lane);
+        float tm = kNegInf;
+#pragma unroll
+        for (int u = 0; u < kVocabU; ++u) {
+            const float m = vec_max<DT>(x.v[u]);
+            tm = __builtin_fmaxf(tm, m);
+            if constexpr (TOP) {
+                const int e0 = elem0<DT>(t.j, u, lane);
+                if (e0 < w && (m > best || best_col < 0)) {
+                    best = __builtin_fmaxf(m, kNegInf);                // NaN only: ordered as -inf
+                    best_col = g.col0[t.s] + e0;
+                }
+            }
+        }
+        add_tile<DT, S1>(st, ref, limit, x, tm, g.c, g.slack);
+    }
+    block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
+    u64 top = 0;
+    if constexpr (TOP) top = select_top<DT>(g, row, best, best_col, a.k, lds_keys, waves, wave, lane);
+    if (g.parts > 1) {
+        const long long slot = row * g.parts + part;
+        if (threadIdx.x == 0) a.part[slot] = make_float4(st.m, st.s, st.s1, 0.0f);
+        if constexpr (TOP) {
+            if (wave == 0 && lane < a.k) a.part_top[slot * a.k + lane] = top;
+        }
+        return;
+    }
+    const RowResult res = row_result(st);
+    if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
+    if constexpr (TOP) {
+        if (wave == 0) write_top(g, a, row, st, res, top, lane);
+    }
+    if constexpr (BOTH) gradient_tiles<DT>(g, a, row, st, res, target, first, step, lane);
+}
+
+// A row's results from its parts: one lane per part for the statistics, one
+// wave per part (in turn) for the lists.
+template <int DT, int NR, bool S1, bool TOP>
+__global__ __launch_bounds__(64 * kVocabWaves) void logprobs_join_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
+    __shared__ u64 lds_keys[TOP ? kVocabWaves * 64 : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int waves = blockDim.x >> 6;
+    const long long row = g.row0 + blockIdx.x;
+    const int target = token_of(a, row, g.col0[g.n]);
+    const float xt = target >= 0 ? logit_at<DT>(g, row, target) : 0.0f;
+    Stats st{kNegInf, 0.0f, 0.0f};
+    if (lane < g.parts) {
+        const float4 p = a.part[row * g.parts + lane];
+        st = Stats{p.x, p.y, p.z};
+    }
+    wave_stats<S1>(st, g.c);
+    const RowResult res = row_result(st);
+    if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
+    if constexpr (TOP) {
+        u64 v = 0;
+        for (int p = wave; p < g.parts; p += waves) {
+            const int i = 63 - lane;
+            const u64 b = i < a.k ? a.part_top[(row * g.parts + p) * a.k + i] : 0;
+            v = merge_lists(v, b, lane);
+        }
+        v = block_lists(v, lds_keys, waves, wave, lane);
+        if (wave == 0) write_top(g, a, row, st, res, v, lane);
+    }
+}
+
+template <int DT, int NR>
+__global__ __launch_bounds__(64 * kVocabWaves) void logprobs_backward_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int waves = blockDim.x >> 6;
+    const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
+    const long long row = g.row0 + local;
+    const float *o = a.saved + row * 4;
+    const Stats st{o[0], o[1], 0.0f};
+    RowResult res;
+    res.empty = st.m == kNegInf && st.s == 0.0f;
+    res.lse = logf(st.s);
+    res.entropy = o[2];
+    gradient_tiles<DT>(g, a, row, st, res, token_of(a, row, g.col0[g.n]), part * waves + wave, waves * g.parts, lane);
+}
+
+template <int DT, int NR>
+hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage stage, hipStream_t s) {
+    const bool s1 = a.entropy || a.saved || a.grad_entropy, top = a.k > 0;
+    if (stage == kBackward) return launch_rows<NR>(c, a, logprobs_backward_kernel<DT, NR>, c.parts, c.waves, 0, s);
+    if (stage == kBoth) {
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true>, 1, c.waves, 0, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true>, 1, c.waves, 0, s);
+    }
+    if (stage == kForward) {
+        if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false>, c.parts, c.waves, 0, s)
+                           : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false>, c.parts, c.waves, 0, s);
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false>, c.parts, c.waves, 0, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, false>, c.parts, c.waves, 0, s);
+    }
+    int w = 1;
+    while (top && w < c.parts && w < kVocabWaves) w *= 2;
+    if (top) return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, true>, 1, w, 0, s)
+                       : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, true>, 1, w, 0, s);
+    return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, false>, 1, w, 0, s)
+              : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, false>, 1, w, 0, s);
+}
+
+hipError_t launch_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage stage, hipStream_t s) {
+    return dispatch_vocab(c, [&](auto dt, auto nr) { return run_logprobs<dt.value, nr.value>(c, a, stage, s); });
+}
+
+}  // namespace ar
