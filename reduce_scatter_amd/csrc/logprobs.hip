@@ -6,9 +6,10 @@
 // alternatives, its largest logit with the vector it stands in.  That costs
 // the stream nothing more, and it is enough: the k largest logits of a row
 // lie in the k lanes whose best logits come first in the (value, column)
-// order, so after the pass the best-of-lane keys are sorted, and only those k
-// lanes' vectors (k / (64 W) of the row) are read again and sorted.  The work
-// is bounded whatever the order of the logits.
+// order, so after the pass the best-of-lane keys are sorted, and every wave
+// reads those of its lanes that are among the k once more (k / (64 W) of the
+// row in all) and sorts what is not below the k-th.  The work is bounded
+// whatever the order of the logits.
 #include "dispatch.hpp"
 #include "vocab_device.hpp"
 #include "vocab_launch.hpp"
@@ -60,26 +61,32 @@ __device__ __forceinline__ void write_top(const VocabGeom<NR> &g, const Logprobs
 // its vector (col < 0: none).
 template <int DT, int NR>
 __device__ __forceinline__ u64 select_top(const VocabGeom<NR> &g, long long row, float best, int col, int k, u64 *lds,
-                                          int waves, int wave, int lane) {
-    constexpr int K = Lanes<DT>::value;
-    const int step = waves * g.parts;
-    const u64 list = block_lists(sort_down(col >= 0 ? top_key(best, col) : 0, lane), lds, waves, wave, lane);
-    const uint32_t floor = (uint32_t)(__shfl(list, k - 1) >> 32);      // no k-th largest logit is below it
+                                          int waves, int wave, int first, int lane) {
+    constexpr int K = Lanes<DT>::value, PER = kVocabU * K;             // a lane's logits in a tile
+    const u64 key = col >= 0 ? top_key(best, col) : 0;
+    const u64 list = block_lists(merge_lists(0, sort_up(key, lane), lane), lds, waves, wave, lane);
+    u64 least = __shfl(list, k - 1);                                   // the k-th best lane's key
+    least = least ? least : 1;
+    const uint32_t least_value = (uint32_t)(least >> 32);              // no k-th largest logit is below it
     u64 mine = 0;
-    for (int j = wave; j < k; j += waves) {
-        const u64 key = __shfl(list, j);
-        if (!key) break;
-        const Place p = place_of<DT>(g, key_col(key));
-        const int u = lane / K;                                        // lanes 0 .. U*K - 1 take one logit each
-        TileWalk t{0, __builtin_amdgcn_readfirstlane(p.t % step)};
-        for (t.settle<DT>(g); t.s < g.n; t.j += step, t.settle<DT>(g)) {
-            const int e = elem0<DT>(t.j, u, p.lane) + lane % K;
+    u64 pending = __ballot(key >= least);
+    while (pending) {                                                  // 64 / PER of this wave's lanes at a time
+        int from = -1;
+#pragma unroll
+        for (int i = 0; i < 64 / PER; ++i) {
+            if (pending && lane / PER == i) from = __builtin_ctzll(pending);
+            pending &= pending - 1;
+        }
+        const int u = lane % PER / K, i = lane % K;
+        TileWalk t;
+        for (bool more = t.start<DT>(g, row, first); more; more = t.move<DT>(g, row, waves * g.parts)) {
+            const int e = elem0<DT>(t.j, u, from) + i;
             u64 cand = 0;
-            if (u < kVocabU && e < width_of<DT>(g, t.s)) {
-                const u64 c = top_key(load1<DT>(row_of<DT>(g, t.s, row), e), g.col0[t.s] + e);
-                if ((uint32_t)(c >> 32) >= floor) cand = c;
+            if (from >= 0 && e < t.w) {
+                cand = top_key(load1<DT>(t.x, e), t.col + e);
+                cand = (uint32_t)(cand >> 32) >= least_value ? cand : 0;
             }
-            if (__any(cand != 0)) mine = merge_lists(mine, reversed(sort_down(cand, lane), lane), lane);
+            if (__any(cand != 0)) mine = merge_lists(mine, sort_up(cand, lane), lane);
         }
     }
     return block_lists(mine, lds, waves, wave, lane);
@@ -95,60 +102,40 @@ __device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const Log
     constexpr int K = Lanes<DT>::value;
     const float gl = a.grad_logprobs && target >= 0 ? a.grad_logprobs[row] : 0.0f;
     const float gh = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
-    const bool zero = res.empty || (gl == 0.0f && gh == 0.0f);
     const float a0 = -(gl + gh * (res.entropy - res.lse)) * g.inv_t / st.s;
     const float a1 = -gh * kLn2 * g.inv_t / st.s;
     const Ref ref = make_ref(st.m, g.c);
-    const Place p = target >= 0 ? place_of<DT>(g, target) : Place{-1, 0, 0, 0};
-    TileWalk t{0, first};
-    int at = first;
-    for (t.settle<DT>(g); t.s < g.n; t.j += step, at += step, t.settle<DT>(g)) {
-        const int w = width_of<DT>(g, t.s);
-        char *out = grad_row_of<DT>(g, t.s, row);
-        Tile<DT> x;
-        if (zero) {
-#pragma unroll
-            for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                for (int i = 0; i < K; ++i) x.v[u].v[i] = 0.0f;
-        } else {
-            load_tile<DT>(x, row_of<DT>(g, t.s, row), t.j, w, lane);
-            if (ref.wide) {
-#pragma unroll
-                for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                    for (int i = 0; i < K; ++i) x.v[u].v[i] = rel(x.v[u].v[i], ref, g.c);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                    for (int i = 0; i < K; ++i) x.v[u].v[i] = __builtin_fmaf(x.v[u].v[i], g.c, -ref.y);
-            }
-            if (gh == 0.0f) {
-#pragma unroll
-                for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                    for (int i = 0; i < K; ++i) x.v[u].v[i] = exp2_fast(x.v[u].v[i]) * a0;
-            } else {
-#pragma unroll
-                for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                    for (int i = 0; i < K; ++i) {
-                        const float tt = x.v[u].v[i];
-                        x.v[u].v[i] = exp2_fast(tt) * __builtin_fmaf(__builtin_fmaxf(tt, kTLow), a1, a0);
-                    }
-            }
-            if (at == p.t && lane == p.lane) {
-#pragma unroll
-                for (int u = 0; u < kVocabU; ++u)
-#pragma unroll
-                    for (int i = 0; i < K; ++i)
-                        if (u == p.u && i == p.i) x.v[u].v[i] += gl * g.inv_t;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kVocabU; ++u) store_vec<DT>(out, x.v[u], elem0<DT>(t.j, u, lane), w);
+    const Place p = target >= 0 ? place_of<DT>(g, target) : Place{-1, 0};
+    if (res.empty || (gl == 0.0f && gh == 0.0f)) {
+        zero_tiles<DT>(g, row, first, step, lane);
+        return;
     }
+    VectorStream<DT, true, NR> stream;
+    stream.start(g, row, first, lane);
+    stream.run(g, row, step, lane, [&](const TileWalk &t, int u, int e0, int held, u32x4 raw) {
+        Pack<DT> x = unpack<DT>(raw);
+        if (ref.wide) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) x.v[i] = (x.v[i] - ref.m) * g.c;
+        } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i) x.v[i] = __builtin_fmaf(x.v[i], g.c, -ref.y);
+        }
+        if (gh == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * a0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                x.v[i] = exp2_fast(x.v[i]) * __builtin_fmaf(hold_up(x.v[i]), a1, a0);
+        }
+        if (t.at == p.t) {
+            const int d = t.j * kTileElems<DT> + p.e - held;
+#pragma unroll
+            for (int i = 0; i < K; ++i) x.v[i] += i == d ? gl * g.inv_t : 0.0f;
+        }
+        store_vec<DT>(grad_row_of<DT>(g, t.s, row), x, t.j, e0, held, t.w);
+    });
 }
 
 __device__ __forceinline__ int token_of(const LogprobsArgs &a, long long row, int vocab) {
@@ -168,36 +155,33 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
     const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
     const long long row = g.row0 + local;
     const int first = part * waves + wave;
+    VectorStream<DT, !BOTH, NR> stream;
+    stream.start(g, row, first, lane);
     const int target = token_of(a, row, g.col0[g.n]);
-    const float xt = target >= 0 && g.parts == 1 ? logit_at<DT>(g, row, target) : 0.0f;
 
-    Stats st{kNegInf, 0.0f, 0.0f};
-    Ref ref = make_ref(kNegInf, g.c);
-    float limit = kNegInf, best = kNegInf;
+    Running run;
+    float best = kNegInf;
     int best_col = -1;
-    TileWalk t{0, first};
-    for (t.settle<DT>(g); t.s < g.n; t.j += step, t.settle<DT>(g)) {
-        const int w = width_of<DT>(g, t.s);
-        Tile<DT> x;
-        load_tile<DT>(x, row_of<DT>(g, t.s, row), t.j, w, lane);
-        float tm = kNegInf;
+    stream.run(g, row, step, lane, [&](const TileWalk &t, int u, int e0, int held, u32x4 raw) {
+        if (!full_tile<DT>(t.j, t.w)) mask_vec<DT>(raw, e0, held, t.w);
+        const Pack<DT> v = unpack<DT>(raw);
+        if constexpr (TOP) {
+            float m = kNegInf;                                                     // NaN: ordered as -inf
 #pragma unroll
-        for (int u = 0; u < kVocabU; ++u) {
-            const float m = vec_max<DT>(x.v[u]);
-            tm = __builtin_fmaxf(tm, m);
-            if constexpr (TOP) {
-                const int e0 = elem0<DT>(t.j, u, lane);
-                if (e0 < w && (m > best || best_col < 0)) {
-                    best = __builtin_fmaxf(m, kNegInf);                // NaN only: ordered as -inf
-                    best_col = g.col0[t.s] + e0;
-                }
+            for (int i = 0; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
+            if (e0 < t.w && (m > best || best_col < 0)) {
+                best = m;
+                best_col = t.col + e0;
             }
         }
-        add_tile<DT, S1>(st, ref, limit, x, tm, g.c, g.slack);
-    }
+        add_vec<DT, S1>(run, v, g.c);
+    });
+    float xt = 0.0f;
+    if (wave == 0 && g.parts == 1 && target >= 0) xt = logit_at<DT>(g, row, target);
+    Stats st = run.st;
     block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
     u64 top = 0;
-    if constexpr (TOP) top = select_top<DT>(g, row, best, best_col, a.k, lds_keys, waves, wave, lane);
+    if constexpr (TOP) top = select_top<DT>(g, row, best, best_col, a.k, lds_keys, waves, wave, first, lane);
     if (g.parts > 1) {
         const long long slot = row * g.parts + part;
         if (threadIdx.x == 0) a.part[slot] = make_float4(st.m, st.s, st.s1, 0.0f);
@@ -229,13 +213,13 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_join_kernel(const V
         const float4 p = a.part[row * g.parts + lane];
         st = Stats{p.x, p.y, p.z};
     }
-    wave_stats<S1>(st, g.c);
+    wave_stats<S1>(st, lane, g.c);
     const RowResult res = row_result(st);
     if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
     if constexpr (TOP) {
         u64 v = 0;
         for (int p = wave; p < g.parts; p += waves) {
-            const int i = 63 - lane;
+            const int i = 63 - lane;                               // ascending
             const u64 b = i < a.k ? a.part_top[(row * g.parts + p) * a.k + i] : 0;
             v = merge_lists(v, b, lane);
         }
@@ -262,23 +246,23 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_backward_kernel(con
 template <int DT, int NR>
 hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage stage, hipStream_t s) {
     const bool s1 = a.entropy || a.saved || a.grad_entropy, top = a.k > 0;
-    if (stage == kBackward) return launch_rows<NR>(c, a, logprobs_backward_kernel<DT, NR>, c.parts, c.waves, 0, s);
+    if (stage == kBackward) return launch_rows<NR>(c, a, logprobs_backward_kernel<DT, NR>, c.parts, c.waves, s);
     if (stage == kBoth) {
-        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true>, 1, c.waves, 0, s)
-                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true>, 1, c.waves, 0, s);
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true>, 1, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true>, 1, c.waves, s);
     }
     if (stage == kForward) {
-        if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false>, c.parts, c.waves, 0, s)
-                           : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false>, c.parts, c.waves, 0, s);
-        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false>, c.parts, c.waves, 0, s)
-                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, false>, c.parts, c.waves, 0, s);
+        if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false>, c.parts, c.waves, s)
+                           : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false>, c.parts, c.waves, s);
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false>, c.parts, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, false>, c.parts, c.waves, s);
     }
     int w = 1;
     while (top && w < c.parts && w < kVocabWaves) w *= 2;
-    if (top) return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, true>, 1, w, 0, s)
-                       : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, true>, 1, w, 0, s);
-    return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, false>, 1, w, 0, s)
-              : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, false>, 1, w, 0, s);
+    if (top) return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, true>, 1, w, s)
+                       : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, true>, 1, w, s);
+    return s1 ? launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, true, false>, 1, w, s)
+              : launch_rows<NR>(c, a, logprobs_join_kernel<DT, NR, false, false>, 1, w, s);
 }
 
 hipError_t launch_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage stage, hipStream_t s) {

@@ -41,6 +41,7 @@ ar_status_t check_shape(const ar_vocab_t *v, Shape &s) {
         if (pitches[r] > 0x7fffffffLL || gpitches[r] > 0x7fffffffLL) return AR_ERR_UNSUPPORTED;
         // byte offsets stay far inside 63 bits
         if (v->rows * std::max(pitches[r], gpitches[r]) > (1LL << 56)) return AR_ERR_UNSUPPORTED;
+        s.c.tiny |= w > 0 && w < (v->dtype == AR_FLOAT32 ? 4 : 8);
         vocab += w;
         tiles += (int)((w + tile - 1) / tile);
     }
@@ -56,15 +57,29 @@ ar_status_t check_shape(const ar_vocab_t *v, Shape &s) {
     s.c.gpitches = gpitches;
     s.c.temperature = v->temperature;
 
-    // Waves per workgroup and workgroups per row: waves up to one tile each,
-    // at most 16; parts only while the rows alone leave compute units idle.
+    // Waves per row, at most one to a tile.  A wave pays about 2 us of set-up
+    // and merging per row, so waves are only added while rows * waves leaves
+    // compute units short of work; measured on 8192 x 131072 bf16 (us) with 1,
+    // 2, 4, 8 waves: 330, 336, 346, 375; on 777 x 50021: 168, 114, 94, 97.
     int waves = 1;
-    while (waves < kVocabWaves && waves * 2 <= tiles) waves *= 2;
+    while (waves < kVocabWaves && waves * 2 <= tiles && v->rows * waves < 16384) waves *= 2;
+    // Workgroups per row, while the rows alone leave compute units idle.
     int parts = 1;
     while (parts < kVocabParts && parts * 2 * waves <= tiles && v->rows * parts * 2 <= 256) parts *= 2;
     s.c.waves = waves;
     s.c.parts = parts;
     return AR_OK;
+}
+
+// The same shape for kernels that come back to a row they have read (its
+// gradient in the same call, its top entries): as many waves as there may be,
+// so that few rows are in flight and the second look finds them in the caches.
+// Measured on 8192 x 131072 bf16 (distillation step, us) with 1, 2, 4, 8
+// waves: 1250, 1192, 931, 920; on 512 x 131072 (top 64): 1064, 336, 149, 85.
+VocabCall short_rows(const Shape &s) {
+    VocabCall c = s.c;
+    while (c.waves < kVocabWaves && c.waves * 2 <= c.tiles && c.parts == 1) c.waves *= 2;
+    return c;
 }
 
 // Workspace: partial statistics, partial lists, statistics for a gradient
@@ -200,7 +215,7 @@ ar_status_t ar_logprobs(const void *const *logits, const ar_vocab_t *shape, cons
         a.part = (float4 *)((char *)workspace + w.part);
         a.part_top = (unsigned long long *)((char *)workspace + w.top);
     }
-    hipError_t e = launch_logprobs(s.c, a, kForward, stream);
+    hipError_t e = launch_logprobs(top_k ? short_rows(s) : s.c, a, kForward, stream);
     if (e == hipSuccess && s.c.parts > 1) e = launch_logprobs(s.c, a, kJoin, stream);
     return hip_status(e);
 }
@@ -254,7 +269,7 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
     a.saved = saved;
     a.grad_logprobs = grad_logprobs;
     a.grad_entropy = grad_entropy;
-    if (s.c.parts == 1) return hip_status(launch_logprobs(s.c, a, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_logprobs(short_rows(s), a, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_logprobs(s.c, a, kForward, stream);
@@ -339,7 +354,7 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     a.saved = saved;
     a.grad_loss = grad_loss;
     const bool tail = mode == AR_TEACHER_TAIL;
-    if (s.c.parts == 1) return hip_status(launch_distill(s.c, a, tail, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_distill(short_rows(s), a, tail, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_distill(s.c, a, tail, kForward, stream);

@@ -7,9 +7,11 @@
 // logit m, t = x*c - y, y = m*c rounded once, is one fused multiply-add per
 // logit and 2^t one instruction; the rounding of y is the same for every
 // logit and cancels in every result, because results only use t and the sum
-// relative to the same y.  A lane's reference moves only when a tile's
-// maximum exceeds it by more than 8 / c (a factor 2^8, far from overflow in
-// fp32), so the rescaling multiply is rare and the sums lose nothing.
+// relative to the same y.  The reference need not be the maximum: a lane takes
+// its first vector's and keeps it while its sum stays below 2^16 (at most 2^14
+// terms of at most 1 if the reference is the maximum), so the stream takes no
+// maxima; a vector that carries the sum past that is added again after moving
+// the reference.
 #pragma once
 
 #include "ar_device.hpp"
@@ -69,42 +71,62 @@ __device__ __forceinline__ void shift_stats(Stats &a, float to, float c) {
     a.m = to;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
+// The value of lane (lane ^ M): data-parallel moves within rows of 16 lanes,
+// gfx950's row swaps across them; none goes through LDS.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int M> __device__ __forceinline__ uint32_t lane_xor(uint32_t v, int lane) {
+    static_assert(M == 1 || M == 2 || M == 4 || M == 8 || M == 16 || M == 32, "one bit");
+    if constexpr (M == 1) return dpp<0xB1>(v);                          // quad_perm 1 0 3 2
+    else if constexpr (M == 2) return dpp<0x4E>(v);                     // quad_perm 2 3 0 1
+    else if constexpr (M == 4) return dpp<0x1B>(dpp<0x141>(v));         // half-row mirror (^7), then ^3
+    else if constexpr (M == 8) return dpp<0x128>(v);                    // row rotate by 8
+    else {
+        // the swaps exchange odd rows (halves) of one register with even rows (halves) of the other
+        if constexpr (M == 16) {
+            const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+            return lane & 16 ? r[0] : r[1];
+        } else {
+            const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+            return lane & 32 ? r[0] : r[1];
+        }
+    }
+}
+// The bits 1, 2, ..., 32 in turn, as compile-time constants.
+template <typename F> __device__ __forceinline__ void each_bit(F f) {
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 8>{});
+    f(std::integral_constant<int, 16>{});
+    f(std::integral_constant<int, 32>{});
+}
+__device__ __forceinline__ float wave_max(float v, int lane) {
+    each_bit([&](auto m) { v = __builtin_fmaxf(v, bits_f32(lane_xor<m.value>(f32_bits(v), lane))); });
     return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+__device__ __forceinline__ float wave_sum(float v, int lane) {
+    each_bit([&](auto m) { v += bits_f32(lane_xor<m.value>(f32_bits(v), lane)); });
     return v;
 }
 
 // Every lane's statistics joined over the wave (all lanes get the result).
-template <bool S1> __device__ __forceinline__ void wave_stats(Stats &a, float c) {
-    shift_stats(a, wave_max(a.m), c);
-    a.s = wave_sum(a.s);
-    if constexpr (S1) a.s1 = wave_sum(a.s1);
+template <bool S1> __device__ __forceinline__ void wave_stats(Stats &a, int lane, float c) {
+    shift_stats(a, wave_max(a.m, lane), c);
+    a.s = wave_sum(a.s, lane);
+    if constexpr (S1) a.s1 = wave_sum(a.s1, lane);
 }
 
-// Joined over the workgroup's waves, in wave order; `lds` holds kVocabWaves
-// entries and may be reused after the next barrier.
+// Joined over the workgroup's waves; `lds` holds kVocabWaves entries and may
+// be reused after the next barrier.
 template <bool S1> __device__ __forceinline__ void block_stats(Stats &a, Stats *lds, int waves, int wave, int lane, float c) {
-    wave_stats<S1>(a, c);
+    wave_stats<S1>(a, lane, c);
     if (waves == 1) return;
     if (lane == 0) lds[wave] = a;
     __syncthreads();
-    Stats r = lds[0];
-    float m = r.m;
-    for (int w = 1; w < waves; ++w) m = __builtin_fmaxf(m, lds[w].m);
-    shift_stats(r, m, c);
-    for (int w = 1; w < waves; ++w) {
-        Stats b = lds[w];
-        shift_stats(b, m, c);
-        r.s += b.s;
-        r.s1 += b.s1;
-    }
-    a = r;
+    a = lane < waves ? lds[lane] : Stats{kNegInf, 0.0f, 0.0f};
+    wave_stats<S1>(a, lane, c);
 }
 
 // ---- the tile walk --------------------------------------------------------
@@ -118,19 +140,6 @@ template <int DT, int NR> __device__ __forceinline__ int tiles_of(const VocabGeo
     return (width_of<DT>(g, s) + kTileElems<DT> - 1) / kTileElems<DT>;
 }
 
-// Tile t as a rank and a tile within it; s == n past the last tile.
-struct TileWalk {
-    int s, j;
-    template <int DT, int NR> __device__ __forceinline__ void settle(const VocabGeom<NR> &g) {
-        while (s < g.n) {
-            const int k = tiles_of<DT>(g, s);
-            if (j < k) break;
-            j -= k;
-            ++s;
-        }
-    }
-};
-
 template <int DT, int NR> __device__ __forceinline__ const char *row_of(const VocabGeom<NR> &g, int s, long long row) {
     return g.x[s] + row * (long long)g.pitch[s] * elem_bytes<DT>();
 }
@@ -138,36 +147,133 @@ template <int DT, int NR> __device__ __forceinline__ char *grad_row_of(const Voc
     return g.g[s] + row * (long long)g.gpitch[s] * elem_bytes<DT>();
 }
 
+// A wave's way through its tiles: the tile (numbered over all ranks), its
+// rank, its number within the rank, and what the rank's tiles have in common.
+struct TileWalk {
+    int at, s, j;
+    int w, tiles, col;                 // the rank's width, tiles and first column
+    const char *x;                     // its logits of the row
+
+    // To the tile `by` further on; false past the last.
+    template <int DT, int NR> __device__ __forceinline__ bool move(const VocabGeom<NR> &g, long long row, int by) {
+        at += by;
+        j += by;
+        if (j < tiles) return true;
+        do {
+            j -= tiles;
+            if (++s >= g.n) return false;
+            tiles = tiles_of<DT>(g, s);
+        } while (j >= tiles);
+        load_rank<DT>(g, row);
+        return true;
+    }
+    template <int DT, int NR> __device__ __forceinline__ bool start(const VocabGeom<NR> &g, long long row, int first) {
+        at = s = j = 0;
+        tiles = tiles_of<DT>(g, 0);
+        load_rank<DT>(g, row);
+        return move<DT>(g, row, first);
+    }
+    template <int DT, int NR> __device__ __forceinline__ void load_rank(const VocabGeom<NR> &g, long long row) {
+        w = width_of<DT>(g, s);
+        col = g.col0[s];
+        x = row_of<DT>(g, s, row);
+    }
+};
+
 // First element (within the rank) of vector u of this lane in tile j.
 template <int DT> __device__ __forceinline__ int elem0(int j, int u, int lane) {
     return ((j * kVocabU + u) * 64 + lane) * Lanes<DT>::value;
 }
+template <int DT> __device__ __forceinline__ bool full_tile(int j, int w) { return (j + 1) * kTileElems<DT> <= w; }
 
-// A tile's logits; past the rank's width -inf.  `w` is the rank's width.
-template <int DT> struct Tile {
-    Pack<DT> v[kVocabU];
-};
-template <int DT> __device__ __forceinline__ void load_tile(Tile<DT> &t, const char *x, int j, int w, int lane) {
+// Where register element 0 of that vector stands.  The vector covers elements
+// [e0, min(e0 + K, w)); past the last whole vector its registers hold the
+// rank's last K elements, of which those before e0 are another vector's, so
+// that one unconditional in-bounds 16-byte load serves every lane of a rank of
+// at least K columns.  Ranks of fewer (TINY) are served by the kernels with
+// the large pointer table alone.
+template <int DT, bool TINY> __device__ __forceinline__ int held0(int e0, int w) {
     constexpr int K = Lanes<DT>::value;
-    if ((j + 1) * kTileElems<DT> <= w) {
-        u32x4 raw[kVocabU];
+    if (TINY && w < K) return e0;
+    return e0 < w - K ? e0 : w - K;
+}
+template <int NR> constexpr bool kTiny = NR > kVocabFew;
+
+template <int DT> __device__ __forceinline__ uint32_t neg_inf_bits() {
+    return DT == F32 ? 0xff800000u : DT == BF16 ? 0xff80u : 0xfc00u;
+}
+// Vector u of a tile.  STREAM: the logits are not read again (non-temporal).
+template <int DT, bool STREAM, bool TINY>
+__device__ __forceinline__ u32x4 load_vec(const TileWalk &t, int u, int lane) {
+    constexpr int K = Lanes<DT>::value;
+    if constexpr (TINY) {
+        if (t.w < K) {                                         // all in vector 0 of lane 0
+            u32x4 v{0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < kVocabU; ++u)
-            raw[u] = *(const u32x4e *)(x + (uint32_t)elem0<DT>(j, u, lane) * elem_bytes<DT>());
-#pragma unroll
-        for (int u = 0; u < kVocabU; ++u) t.v[u] = unpack<DT>(raw[u]);
-    } else {
-#pragma unroll
-        for (int u = 0; u < kVocabU; ++u) {
-            const int e0 = elem0<DT>(j, u, lane);
-            if (e0 + K <= w) t.v[u] = unpack<DT>(*(const u32x4e *)(x + (uint32_t)e0 * elem_bytes<DT>()));
-            else {
-#pragma unroll
-                for (int i = 0; i < K; ++i) t.v[u].v[i] = e0 + i < w ? load1<DT>(x, e0 + i) : kNegInf;
+            for (int i = 0; i < K; ++i) {
+                if (lane == 0 && u == 0 && i < t.w) {
+                    if constexpr (DT == F32) v[i] = ((const uint32_t *)t.x)[i];
+                    else v[i / 2] |= (uint32_t)((const uint16_t *)t.x)[i] << (i & 1) * 16;
+                }
             }
+            return v;
+        }
+    }
+    // in bytes, from the lane's part and the wave's, so that two instructions make the address
+    const uint32_t at = (uint32_t)lane * 16u + (uint32_t)elem0<DT>(t.j, u, 0) * elem_bytes<DT>();
+    const uint32_t last = (uint32_t)(t.w - K) * elem_bytes<DT>();
+    const u32x4e *p = (const u32x4e *)(t.x + (at < last ? at : last));
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+// Registers of a vector at a rank's end that hold no element of it become -inf.
+template <int DT> __device__ __forceinline__ void mask_vec(u32x4 &v, int e0, int held, int w) {
+    constexpr int K = Lanes<DT>::value;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const bool out = held + i < e0 || held + i >= w;
+        if constexpr (DT == F32) v[i] = out ? neg_inf_bits<DT>() : v[i];
+        else {
+            const uint32_t part = 0xffffu << (i & 1) * 16, ninf = neg_inf_bits<DT>() << (i & 1) * 16;
+            v[i / 2] = out ? (v[i / 2] & ~part) | ninf : v[i / 2];
         }
     }
 }
+
+// A wave's vectors in order.  start() issues the loads of the first tile, so
+// that what else a kernel has to read and work out runs meanwhile; run() calls
+// f(walk, u, e0, held, raw) for every vector and loads one of the next tile as
+// soon as the one in its registers is used up: a tile's loads stay in flight.
+template <int DT, bool STREAM, int NR> struct VectorStream {
+    static constexpr bool TINY = kTiny<NR>;
+    TileWalk t;
+    u32x4 v[kVocabU];
+    bool any;
+    __device__ __forceinline__ void start(const VocabGeom<NR> &g, long long row, int first, int lane) {
+        any = t.start<DT>(g, row, first);
+        if (!any) return;
+#pragma unroll
+        for (int u = 0; u < kVocabU; ++u) v[u] = load_vec<DT, STREAM, TINY>(t, u, lane);
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(const VocabGeom<NR> &g, long long row, int step, int lane, F f) {
+        // The last round loads its own tile again, into registers that nothing
+        // reads: without a branch around the loads the compiler knows how many
+        // are in flight and waits for the oldest only.
+        for (bool more = any; more;) {
+            TileWalk n = t;
+            more = n.move<DT>(g, row, step);
+            if (!more) n = t;
+#pragma unroll
+            for (int u = 0; u < kVocabU; ++u) {
+                const int e0 = elem0<DT>(t.j, u, lane);
+                f(t, u, e0, held0<DT, TINY>(e0, t.w), v[u]);
+                v[u] = load_vec<DT, STREAM, TINY>(n, u, lane);
+            }
+            t = n;
+        }
+    }
+};
 
 // A vector of gradients, rounded to the logits' type.
 template <int DT> __device__ __forceinline__ u32x4 round_pack(const Pack<DT> &p) {
@@ -185,21 +291,49 @@ template <int DT> __device__ __forceinline__ u32x4 round_pack(const Pack<DT> &p)
     }
     return w;
 }
-template <int DT> __device__ __forceinline__ void store_vec(char *g, const Pack<DT> &p, int e0, int w) {
+// Store a vector whose register 0 stands at element `held`: whole, or at a
+// rank's end only the elements from e0 on (the others are another vector's).
+template <int DT>
+__device__ __forceinline__ void store_vec(char *g, const Pack<DT> &p, int j, int e0, int held, int w) {
     constexpr int K = Lanes<DT>::value;
-    if (e0 + K <= w) {
+    if (full_tile<DT>(j, w) || e0 + K <= w) {
         __builtin_nontemporal_store(round_pack<DT>(p), (u32x4e *)(g + (uint32_t)e0 * elem_bytes<DT>()));
     } else {
 #pragma unroll
         for (int i = 0; i < K; ++i)
-            if (e0 + i < w) store1<DT>(g, e0 + i, round_to<DT>(p.v[i]));
+            if (held + i >= e0 && held + i < w) store1<DT>(g, held + i, round_to<DT>(p.v[i]));
     }
 }
 
+template <int DT, int NR>
+__device__ __forceinline__ void zero_tiles(const VocabGeom<NR> &g, long long row, int first, int step, int lane) {
+    Pack<DT> zero;
+#pragma unroll
+    for (int i = 0; i < Lanes<DT>::value; ++i) zero.v[i] = 0.0f;
+    TileWalk t;
+    for (bool more = t.start<DT>(g, row, first); more; more = t.move<DT>(g, row, step)) {
+#pragma unroll
+        for (int u = 0; u < kVocabU; ++u) {
+            const int e0 = elem0<DT>(t.j, u, lane);
+            store_vec<DT>(grad_row_of<DT>(g, t.s, row), zero, t.j, e0, held0<DT, kTiny<NR>>(e0, t.w), t.w);
+        }
+    }
+}
+
+// f(r) for every rank but the first, without a loop in the kernels with the
+// small table (their first columns are then loaded together).
+template <int NR, typename F> __device__ __forceinline__ void each_later_rank(const VocabGeom<NR> &g, F f) {
+    if constexpr (NR <= kVocabFew) {
+#pragma unroll
+        for (int r = 1; r < NR; ++r) f(r);
+    } else {
+        for (int r = 1; r < g.n; ++r) f(r);
+    }
+}
 // Column id's rank: ranks of no columns are passed over.
 template <int NR> __device__ __forceinline__ int rank_of(const VocabGeom<NR> &g, int id) {
     int s = 0;
-    for (int r = 0; r + 1 < g.n; ++r) s += id >= g.col0[r + 1];
+    each_later_rank(g, [&](int r) { s += id >= g.col0[r]; });
     return s;
 }
 template <int DT, int NR> __device__ __forceinline__ float logit_at(const VocabGeom<NR> &g, long long row, int id) {
@@ -207,65 +341,64 @@ template <int DT, int NR> __device__ __forceinline__ float logit_at(const VocabG
     return load1<DT>(row_of<DT>(g, s, row), id - g.col0[s]);
 }
 
-// The tile, vector, lane and element that hold column id.
+// Column id's tile and its element there, counted from the tile's first.
 struct Place {
-    int t, u, lane, i;
+    int t, e;
 };
 template <int DT, int NR> __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, int id) {
-    constexpr int K = Lanes<DT>::value;
-    int s = 0, t = 0;
-    for (int r = 0; r + 1 < g.n; ++r) {
-        const bool past = id >= g.col0[r + 1];
-        s += past;
-        t += past ? tiles_of<DT>(g, r) : 0;
-    }
-    const int e = id - g.col0[s], c = e / K;
-    return {t + c / (64 * kVocabU), (c / 64) % kVocabU, c % 64, e % K};
+    int first = 0, t = 0;
+    each_later_rank(g, [&](int r) {
+        const bool past = id >= g.col0[r];
+        first = past ? g.col0[r] : first;
+        t += past ? tiles_of<DT>(g, r - 1) : 0;
+    });
+    const int e = id - first;
+    return {t + e / kTileElems<DT>, e % kTileElems<DT>};
 }
 
-// Move a lane's reference to cover a tile whose maximum is tm.
-__device__ __forceinline__ void rebase(Stats &a, Ref &r, float &limit, float tm, float c, float slack) {
-    if (tm > limit) {
-        shift_stats(a, tm, c);
-        r = make_ref(tm, c);
-        limit = tm + slack;
-    }
+// A lane's running sums and reference.
+struct Running {
+    Stats st{kNegInf, 0.0f, 0.0f};
+    Ref ref{kNegInf, 0.0f, false};
+    int slow = 1;                      // some lane has met no logit above -inf yet, or its reference is wide
+};
+// max(t, kTLow) as one instruction: the builtin first quiets a signalling
+// NaN, which no result of arithmetic is.
+__device__ __forceinline__ float hold_up(float t) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "s"(kTLow), "v"(t));
+    return r;
 }
-
-// Add one vector's logits to a lane's sums.
-template <int DT, bool S1> __device__ __forceinline__ void add_vec(Stats &a, const Ref &r, const Pack<DT> &v, float c) {
+// Add one vector's logits to a lane's sums (SLOW: any reference).  2^t = 0
+// where t = -inf, but 0 * -inf is NaN: t is held above kTLow in the weighted
+// sum.
+template <int DT, bool S1, bool SLOW> __device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v, float c) {
 #pragma unroll
     for (int i = 0; i < Lanes<DT>::value; ++i) {
-        const float t = __builtin_fmaf(v.v[i], c, -r.y);
+        const float t = SLOW ? rel(v.v[i], a.ref, c) : __builtin_fmaf(v.v[i], c, -a.ref.y);
         const float e = exp2_fast(t);
-        a.s += e;
-        if constexpr (S1) a.s1 = __builtin_fmaf(e, __builtin_fmaxf(t, kTLow), a.s1);
+        a.st.s += e;
+        if constexpr (S1) a.st.s1 = __builtin_fmaf(e, hold_up(t), a.st.s1);
     }
 }
-template <int DT, bool S1> __device__ __forceinline__ void add_vec_wide(Stats &a, const Ref &r, const Pack<DT> &v, float c) {
+template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, float c) {
+    const Stats before = a.st;
+    add_terms<DT, S1, false>(a, x, c);
+    if (__ballot(a.st.s > 65536.0f) | (u64)a.slow) {                 // the first vector, and seldom again: add it with care
+        a.st = before;
+        Pack<DT> v = x;
+        // other values to the compiler, which would otherwise take the first steps below for every vector
 #pragma unroll
-    for (int i = 0; i < Lanes<DT>::value; ++i) {
-        const float t = rel(v.v[i], r, c);
-        const float e = exp2_fast(t);
-        a.s += e;
-        if constexpr (S1) a.s1 = __builtin_fmaf(e, __builtin_fmaxf(t, kTLow), a.s1);
-    }
-}
-template <int DT> __device__ __forceinline__ float vec_max(const Pack<DT> &v) {
-    float m = v.v[0];
+        for (int i = 0; i < Lanes<DT>::value; ++i) asm volatile("" : "+v"(v.v[i]));
+        float m = v.v[0];
 #pragma unroll
-    for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
-    return m;
-}
-template <int DT, bool S1> __device__ __forceinline__ void add_tile(Stats &a, Ref &r, float &limit, const Tile<DT> &t,
-                                                                    float tm, float c, float slack) {
-    if (__any(tm > limit)) rebase(a, r, limit, tm, c, slack);
-    if (__any(r.wide)) {
-#pragma unroll
-        for (int u = 0; u < kVocabU; ++u) add_vec_wide<DT, S1>(a, r, t.v[u], c);
-    } else {
-#pragma unroll
-        for (int u = 0; u < kVocabU; ++u) add_vec<DT, S1>(a, r, t.v[u], c);
+        for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
+        if (m > a.st.m) {
+            shift_stats(a.st, m, c);
+            a.ref = make_ref(m, c);
+        }
+        a.slow = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf || a.ref.wide));
+        add_terms<DT, S1, true>(a, v, c);
     }
 }
 
@@ -284,33 +417,32 @@ __device__ __forceinline__ float order_value(uint32_t o) {
 __device__ __forceinline__ u64 top_key(float x, int col) { return (u64)order_bits(x) << 32 | (uint32_t)~col; }
 __device__ __forceinline__ int key_col(u64 k) { return (int)~(uint32_t)k; }
 
-__device__ __forceinline__ u64 shfl_xor64(u64 v, int mask) {
-    const uint32_t lo = __shfl_xor((uint32_t)v, mask), hi = __shfl_xor((uint32_t)(v >> 32), mask);
-    return (u64)hi << 32 | lo;
-}
-__device__ __forceinline__ u64 cmp_exchange(u64 v, int mask, bool keep_max) {
-    const u64 o = shfl_xor64(v, mask);
+template <int M> __device__ __forceinline__ u64 cmp_exchange(u64 v, int lane, bool keep_max) {
+    const uint32_t lo = lane_xor<M>((uint32_t)v, lane), hi = lane_xor<M>((uint32_t)(v >> 32), lane);
+    const u64 o = (u64)hi << 32 | lo;
     return (o > v) == keep_max ? o : v;
 }
-// A bitonic sequence over the 64 lanes into descending order.
-__device__ __forceinline__ u64 merge_down(u64 v, int lane) {
-#pragma unroll
-    for (int j = 32; j; j >>= 1) v = cmp_exchange(v, j, !(lane & j));
+// A bitonic sequence over blocks of 2 * M lanes into order: descending in
+// lanes where `down`.
+template <int M> __device__ __forceinline__ u64 merge_steps(u64 v, int lane, bool down) {
+    v = cmp_exchange<M>(v, lane, !(lane & M) == down);
+    if constexpr (M > 1) v = merge_steps<M / 2>(v, lane, down);
     return v;
 }
-__device__ __forceinline__ u64 sort_down(u64 v, int lane) {
-#pragma unroll
-    for (int k = 2; k < 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j; j >>= 1) v = cmp_exchange(v, j, !(lane & j) == !(lane & k));
-    return merge_down(v, lane);
+// The 64 lanes' keys in ascending order.
+__device__ __forceinline__ u64 sort_up(u64 v, int lane) {
+    v = merge_steps<1>(v, lane, (lane & 2) != 0);
+    v = merge_steps<2>(v, lane, (lane & 4) != 0);
+    v = merge_steps<4>(v, lane, (lane & 8) != 0);
+    v = merge_steps<8>(v, lane, (lane & 16) != 0);
+    v = merge_steps<16>(v, lane, (lane & 32) != 0);
+    return merge_steps<32>(v, lane, false);
 }
-// The 64 largest of two descending lists, descending: lane i keeps the larger
-// of a[i] and b[63 - i], which is a bitonic sequence.
-__device__ __forceinline__ u64 merge_lists(u64 a, u64 b_reversed, int lane) {
-    return merge_down(a > b_reversed ? a : b_reversed, lane);
+// The 64 largest of a descending and an ascending list, descending: lane i
+// keeps the larger of a[i] and the i-th smallest of b, a bitonic sequence.
+__device__ __forceinline__ u64 merge_lists(u64 down, u64 up, int lane) {
+    return merge_steps<32>(down > up ? down : up, lane, true);
 }
-__device__ __forceinline__ u64 reversed(u64 v, int lane) { return shfl_xor64(v, 63); }
 
 // The 64 largest of every wave's descending list, in all waves.  `lds` holds
 // waves * 64 keys.

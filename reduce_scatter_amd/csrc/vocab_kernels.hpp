@@ -15,7 +15,7 @@
 namespace ar {
 
 constexpr int kVocabU = 4;             // 16-byte vectors per lane and tile
-constexpr int kVocabWaves = 16;        // most waves per workgroup
+constexpr int kVocabWaves = 8;         // most waves per workgroup
 constexpr int kVocabParts = 32;        // most workgroups per row
 constexpr int kVocabFew = 16;          // ranks of the small pointer table
 constexpr int kVocabMany = 128;        // ranks of the large one
@@ -26,11 +26,10 @@ template <int NR> struct VocabGeom {
     const char *x[NR];                 // logits of each rank
     char *g[NR];                       // gradients (unused by forward kernels)
     uint32_t pitch[NR], gpitch[NR];    // elements between rows
-    int col0[NR + 1];                  // first column of each rank; col0[n] = V
+    int col0[NR + 1];                  // first column of each rank; V from col0[n] on
     int n, parts;
     float c;                           // log2(e) / T
     float inv_t;                       // 1 / T
-    float slack;                       // 8 / c: a maximum this far above the reference moves it
     long long row0;                    // first row of this launch
 };
 
@@ -59,6 +58,7 @@ struct VocabCall {
     int dtype;                         // ar::Dtype
     long long rows;
     int n, tiles, parts, waves;
+    bool tiny;                         // a rank has columns, but not enough for one vector
     const void *const *x;
     void *const *g;                    // nullptr for forward calls
     const long long *widths, *pitches, *gpitches;

@@ -22,25 +22,24 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
         g.col0[r] = col;
         col += (int)c.widths[r];
     }
-    g.col0[c.n] = col;
+    for (int r = c.n; r <= NR; ++r) g.col0[r] = col;           // no column is past them
     g.n = c.n;
     g.parts = c.parts;
     g.c = (float)(1.4426950408889634 / (double)c.temperature);
     g.inv_t = (float)(1.0 / (double)c.temperature);
-    g.slack = (float)(8.0 * 0.6931471805599453 * (double)c.temperature);
 }
 
 // One workgroup of ``waves`` waves for each of ``per_row`` parts of every row.
-template <int NR, typename A, typename... X>
-hipError_t launch_rows(const VocabCall &c, const A &a, void (*k)(const VocabGeom<NR>, const A, const X...), int per_row,
-                       int waves, size_t lds, hipStream_t s, const X &...extra) {
+template <int NR, typename A>
+hipError_t launch_rows(const VocabCall &c, const A &a, void (*k)(const VocabGeom<NR>, const A), int per_row, int waves,
+                       hipStream_t s) {
     VocabGeom<NR> g;
     fill_geom(c, g);
     const long long most = kVocabGridThreads / (64LL * waves * per_row);
     for (long long row = 0; row < c.rows; row += most) {
         g.row0 = row;
         const long long n = c.rows - row < most ? c.rows - row : most;
-        const hipError_t e = launch(k, dim3((unsigned)(n * per_row)), dim3(64u * (unsigned)waves), lds, s, g, a, extra...);
+        const hipError_t e = launch(k, dim3((unsigned)(n * per_row)), dim3(64u * (unsigned)waves), 0, s, g, a);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -48,7 +47,7 @@ hipError_t launch_rows(const VocabCall &c, const A &a, void (*k)(const VocabGeom
 
 template <typename F> hipError_t dispatch_vocab(const VocabCall &c, F &&f) {
     auto by_n = [&](auto dt) {
-        return c.n <= kVocabFew ? f(dt, std::integral_constant<int, kVocabFew>{})
+        return c.n <= kVocabFew && !c.tiny ? f(dt, std::integral_constant<int, kVocabFew>{})
                                 : f(dt, std::integral_constant<int, kVocabMany>{});
     };
     switch (c.dtype) {
