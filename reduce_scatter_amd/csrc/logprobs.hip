@@ -8,8 +8,9 @@
 // lie in the k lanes whose best logits come first in the (value, column)
 // order, so after the pass the best-of-lane keys are sorted, and every wave
 // reads those of its lanes that are among the k once more (k / (64 W) of the
-// row in all) and sorts what is not below the k-th.  The work is bounded
-// whatever the order of the logits.
+// row in all); what is not below the k-th of them, seldom much more than k
+// logits, is collected and sorted.  The work is bounded whatever the order of
+// the logits.
 #include "dispatch.hpp"
 #include "vocab_device.hpp"
 #include "vocab_launch.hpp"
@@ -48,48 +49,127 @@ __device__ __forceinline__ void write_row(const VocabGeom<NR> &g, const Logprobs
 
 template <int NR>
 __device__ __forceinline__ void write_top(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row, const Stats &st,
-                                          const RowResult &res, u64 key, int lane) {
-    if (lane >= a.k) return;
+                                          const RowResult &res, u64 key, int i) {
     const Ref ref = make_ref(st.m, g.c);
     const float x = order_value((uint32_t)(key >> 32));
-    a.top_ids[row * a.k + lane] = key ? (int64_t)key_col(key) : -1;
-    a.top_logprobs[row * a.k + lane] = !key || res.empty ? kNegInf : rel_ln(x, ref, g.c, g.inv_t) - res.lse;
+    a.top_ids[row * a.k + i] = key ? (int64_t)key_col(key) : -1;
+    a.top_logprobs[row * a.k + i] = !key || res.empty ? kNegInf : rel_ln(x, ref, g.c, g.inv_t) - res.lse;
 }
 
-// The 64 largest keys of this workgroup's part of the row, of which the first
-// k are exact; best / col: each lane's largest logit and the first column of
-// its vector (col < 0: none).
-template <int DT, int NR>
-__device__ __forceinline__ u64 select_top(const VocabGeom<NR> &g, long long row, float best, int col, int k, u64 *lds,
-                                          int waves, int wave, int first, int lane) {
-    constexpr int K = Lanes<DT>::value, PER = kVocabU * K;             // a lane's logits in a tile
-    const u64 key = col >= 0 ? top_key(best, col) : 0;
-    const u64 list = block_lists(merge_lists(0, sort_up(key, lane), lane), lds, waves, wave, lane);
-    u64 least = __shfl(list, k - 1);                                   // the k-th best lane's key
-    least = least ? least : 1;
-    const uint32_t least_value = (uint32_t)(least >> 32);              // no k-th largest logit is below it
-    u64 mine = 0;
-    u64 pending = __ballot(key >= least);
-    while (pending) {                                                  // 64 / PER of this wave's lanes at a time
-        int from = -1;
+// f(keys) with those keys (0: none) that are not below `least` among the
+// logits of this wave's lanes in `pending`.  A load takes the vectors of two
+// of those lanes in eight tiles (a vector to a lane), four loads at a time are
+// in flight, and where the tiles lie is worked out once for all of them.
+template <int DT, int NR, typename F>
+__device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, u64 lanes, u64 least, int first,
+                                         int step, int lane, F f) {
+    constexpr int K = Lanes<DT>::value, kAhead = 4;
+    const float floor = order_value((uint32_t)(least >> 32));
+    const int half = lane >> 5, tile = (lane & 31) / kVocabU, u = lane % kVocabU;
+    for (int base = first; base < g.tiles; base += 8 * step) {
+        int t = base + tile * step, s = 0, before = 0, tiles = 0;
+        each_later_rank(g, [&](int r) {
+            tiles += tiles_of<DT>(g, r - 1);
+            s = t >= tiles ? r : s;
+            before = t >= tiles ? tiles : before;
+        });
+        const bool there = t < g.tiles;
+        s = there ? s : 0;
+        const int w = there ? width_of<DT>(g, s) : 0, col = g.col0[s];
+        const char *x = row_of<DT>(g, s, row);
+        const int j = t - before;
+        for (u64 pending = lanes; pending;) {
+            u32x4 v[kAhead];
+            int e0[kAhead];
 #pragma unroll
-        for (int i = 0; i < 64 / PER; ++i) {
-            if (pending && lane / PER == i) from = __builtin_ctzll(pending);
-            pending &= pending - 1;
-        }
-        const int u = lane % PER / K, i = lane % K;
-        TileWalk t;
-        for (bool more = t.start<DT>(g, row, first); more; more = t.move<DT>(g, row, waves * g.parts)) {
-            const int e = elem0<DT>(t.j, u, from) + i;
-            u64 cand = 0;
-            if (from >= 0 && e < t.w) {
-                cand = top_key(load1<DT>(t.x, e), t.col + e);
-                cand = (uint32_t)(cand >> 32) >= least_value ? cand : 0;
+            for (int b = 0; b < kAhead; ++b) {
+                const int one = pending ? __builtin_ctzll(pending) : -1;
+                pending &= pending - 1;
+                const int two = pending ? __builtin_ctzll(pending) : -1;
+                pending &= pending - 1;
+                const int from = half ? two : one;
+                e0[b] = elem0<DT>(j, u, from);
+                if (from < 0 || e0[b] >= w) {
+                    e0[b] = -1;
+                } else if (kTiny<NR> && w < K) {
+                    v[b] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        if (i >= w) continue;
+                        if constexpr (DT == F32) v[b][i] = ((const uint32_t *)x)[i];
+                        else v[b][i / 2] |= (uint32_t)((const uint16_t *)x)[i] << (i & 1) * 16;
+                    }
+                } else {
+                    v[b] = *(const u32x4e *)(x + (uint32_t)held0<DT, false>(e0[b], w) * elem_bytes<DT>());
+                }
             }
-            if (__any(cand != 0)) mine = merge_lists(mine, sort_up(cand, lane), lane);
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b) {
+                const Pack<DT> z = unpack<DT>(v[b]);
+                const int held = held0<DT, kTiny<NR>>(e0[b], w);
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    if (!__any(e0[b] >= 0 && !(z.v[i] < floor))) continue;
+                    u64 key = top_key(z.v[i], col + held + i);
+                    if (e0[b] < 0 || held + i < e0[b] || held + i >= w || key < least) key = 0;
+                    if (__any(key != 0)) f(key);
+                }
+            }
         }
     }
-    return block_lists(mine, lds, waves, wave, lane);
+}
+
+struct TopScratch {
+    u64 keys[kVocabWaves * 64];
+    u64 last;                          // the k-th best lane's key
+    int count;                         // keys collected
+};
+
+// emit(i, key) for the i-th largest key (0: none) of this workgroup's part of
+// the row, i < k; best / col: each lane's largest logit and the first column
+// of its vector (col < 0: none).
+template <int DT, int NR, typename F>
+__device__ __forceinline__ void select_top(const VocabGeom<NR> &g, long long row, float best, int col, int k,
+                                           TopScratch &lds, int waves, int wave, int first, int lane, F emit) {
+    const int step = waves * g.parts, room = waves * 64, thread = wave * 64 + lane;
+    // the k-th best lane: every wave's lanes in order, and for each its rank among all
+    const u64 key = col >= 0 ? top_key(best, col) : 0;
+    const u64 mine = sort_down(key, lane);
+    lds.keys[thread] = mine;
+    for (int i = thread + room; i < kVocabWaves * 64; i += room) lds.keys[i] = 0;
+    if (thread == 0) lds.last = 0, lds.count = 0;
+    __syncthreads();
+    if (lane < k && mine && count_larger<kVocabWaves>(lds.keys, mine) == k - 1) lds.last = mine;
+    __syncthreads();
+    const u64 last = lds.last;
+    // its logit stands in that vector, so k logits at least have keys from here on
+    const u64 least = last ? last - (Lanes<DT>::value - 1) : 1;
+    const u64 lanes = __ballot(key != 0 && key >= last);
+    each_key<DT>(g, row, lanes, least, first, step, lane, [&](u64 v) {
+        if (v) {
+            const int at = atomicAdd(&lds.count, 1);
+            if (at < room) lds.keys[at] = v;
+        }
+    });
+    __syncthreads();
+    const int n = lds.count;
+    if (n <= room) {                                                   // rank them by counting
+        const u64 v = thread < n ? lds.keys[thread] : 0;
+        int rank = 0;
+        for (int i = 0; i < n; i += 8) {
+#pragma unroll
+            for (int b = 0; b < 8; ++b) rank += (lds.keys[i + b] > v) & (i + b < n);    // the array's length is a multiple of 8
+        }
+        if (thread < n && rank < k) emit(rank, v);
+        if (thread >= n && thread < k) emit(thread, 0);
+        return;
+    }
+    // more than fit (long runs of logits in order): every wave keeps the 64 largest of its own
+    u64 v = 0;
+    each_key<DT>(g, row, lanes, least, first, step, lane,
+                 [&](u64 c) { v = merge_lists(v, reversed(sort_down(c, lane), lane), lane); });
+    v = block_lists(v, lds.keys, waves, wave, lane);
+    if (thread < k) emit(thread, v);
 }
 
 // Gradient of this workgroup's tiles: with e = 2^t and p = e / S,
@@ -149,7 +229,6 @@ __device__ __forceinline__ int token_of(const LogprobsArgs &a, long long row, in
 template <int DT, int NR, bool S1, bool TOP, bool BOTH>
 __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
     __shared__ Stats lds_stats[kVocabWaves];
-    __shared__ u64 lds_keys[TOP ? kVocabWaves * 64 : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int waves = blockDim.x >> 6, step = waves * g.parts;
     const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
@@ -180,20 +259,18 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
     if (wave == 0 && g.parts == 1 && target >= 0) xt = logit_at<DT>(g, row, target);
     Stats st = run.st;
     block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
-    u64 top = 0;
-    if constexpr (TOP) top = select_top<DT>(g, row, best, best_col, a.k, lds_keys, waves, wave, first, lane);
-    if (g.parts > 1) {
-        const long long slot = row * g.parts + part;
-        if (threadIdx.x == 0) a.part[slot] = make_float4(st.m, st.s, st.s1, 0.0f);
-        if constexpr (TOP) {
-            if (wave == 0 && lane < a.k) a.part_top[slot * a.k + lane] = top;
-        }
-        return;
-    }
     const RowResult res = row_result(st);
-    if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
+    const long long slot = row * g.parts + part;
+    if (threadIdx.x == 0) {
+        if (g.parts > 1) a.part[slot] = make_float4(st.m, st.s, st.s1, 0.0f);
+        else write_row(g, a, row, st, res, xt, target >= 0);
+    }
     if constexpr (TOP) {
-        if (wave == 0) write_top(g, a, row, st, res, top, lane);
+        __shared__ TopScratch lds_top;
+        select_top<DT>(g, row, best, best_col, a.k, lds_top, waves, wave, first, lane, [&](int i, u64 key) {
+            if (g.parts > 1) a.part_top[slot * a.k + i] = key;
+            else write_top(g, a, row, st, res, key, i);
+        });
     }
     if constexpr (BOTH) gradient_tiles<DT>(g, a, row, st, res, target, first, step, lane);
 }
@@ -224,7 +301,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_join_kernel(const V
             v = merge_lists(v, b, lane);
         }
         v = block_lists(v, lds_keys, waves, wave, lane);
-        if (wave == 0) write_top(g, a, row, st, res, v, lane);
+        if (wave == 0 && lane < a.k) write_top(g, a, row, st, res, v, lane);
     }
 }
 

@@ -429,17 +429,24 @@ template <int M> __device__ __forceinline__ u64 merge_steps(u64 v, int lane, boo
     if constexpr (M > 1) v = merge_steps<M / 2>(v, lane, down);
     return v;
 }
-// The 64 lanes' keys in ascending order.
-__device__ __forceinline__ u64 sort_up(u64 v, int lane) {
-    v = merge_steps<1>(v, lane, (lane & 2) != 0);
-    v = merge_steps<2>(v, lane, (lane & 4) != 0);
-    v = merge_steps<4>(v, lane, (lane & 8) != 0);
-    v = merge_steps<8>(v, lane, (lane & 16) != 0);
-    v = merge_steps<16>(v, lane, (lane & 32) != 0);
-    return merge_steps<32>(v, lane, false);
+// The 64 lanes' keys in descending order.
+__device__ __forceinline__ u64 sort_down(u64 v, int lane) {
+    v = merge_steps<1>(v, lane, !(lane & 2));
+    v = merge_steps<2>(v, lane, !(lane & 4));
+    v = merge_steps<4>(v, lane, !(lane & 8));
+    v = merge_steps<8>(v, lane, !(lane & 16));
+    v = merge_steps<16>(v, lane, !(lane & 32));
+    return merge_steps<32>(v, lane, true);
+}
+// The reverse of the lanes' order.
+__device__ __forceinline__ u64 reversed(u64 v, int lane) {
+    uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+    lo = lane_xor<32>(lane_xor<16>(dpp<0x140>(lo), lane), lane);        // row mirror (^15), ^16, ^32
+    hi = lane_xor<32>(lane_xor<16>(dpp<0x140>(hi), lane), lane);
+    return (u64)hi << 32 | lo;
 }
 // The 64 largest of a descending and an ascending list, descending: lane i
-// keeps the larger of a[i] and the i-th smallest of b, a bitonic sequence.
+// keeps the larger of the two, which makes a bitonic sequence.
 __device__ __forceinline__ u64 merge_lists(u64 down, u64 up, int lane) {
     return merge_steps<32>(down > up ? down : up, lane, true);
 }
@@ -459,6 +466,21 @@ __device__ __forceinline__ u64 block_lists(u64 v, u64 *lds, int waves, int wave,
         __syncthreads();
     }
     return lds[lane];
+}
+
+// How many keys of N descending lists of 64 in LDS are larger than v: a binary
+// search in each, all at once, because every step waits for LDS.
+template <int N> __device__ __forceinline__ int count_larger(const u64 *lists, u64 v) {
+    int n[N], all = 0;
+#pragma unroll
+    for (int w = 0; w < N; ++w) n[w] = 0;
+#pragma unroll
+    for (int b = 32; b; b >>= 1)
+#pragma unroll
+        for (int w = 0; w < N; ++w) n[w] += lists[w * 64 + n[w] + b - 1] > v ? b : 0;
+#pragma unroll
+    for (int w = 0; w < N; ++w) all += n[w] + (lists[w * 64 + n[w]] > v);
+    return all;
 }
 
 }  // namespace ar

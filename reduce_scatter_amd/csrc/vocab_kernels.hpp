@@ -28,6 +28,7 @@ template <int NR> struct VocabGeom {
     uint32_t pitch[NR], gpitch[NR];    // elements between rows
     int col0[NR + 1];                  // first column of each rank; V from col0[n] on
     int n, parts;
+    int tiles;                         // of the row, over all ranks
     float c;                           // log2(e) / T
     float inv_t;                       // 1 / T
     long long row0;                    // first row of this launch

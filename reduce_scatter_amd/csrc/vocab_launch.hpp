@@ -25,6 +25,7 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
     for (int r = c.n; r <= NR; ++r) g.col0[r] = col;           // no column is past them
     g.n = c.n;
     g.parts = c.parts;
+    g.tiles = c.tiles;
     g.c = (float)(1.4426950408889634 / (double)c.temperature);
     g.inv_t = (float)(1.0 / (double)c.temperature);
 }
