@@ -109,7 +109,7 @@ __device__ __forceinline__ float row_loss(const VocabGeom<NR> &g, const Teacher<
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const float lp = empty ? kNegInf : rel_ln(z[i], ref, g.c, g.inv_t) - lse;
+        const float lp = empty ? kNegInf : rel_ln(z[i], ref, g.inv_t) - lse;
         if (t.id[i] >= 0 && t.q[i] != 0.0f) sum += t.q[i] * (t.lq[i] - lp);
     }
     sum = wave_sum(sum, lane);
@@ -244,9 +244,8 @@ __device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const Dis
     for (int i = 0; i < PER; ++i) {
         z[i] = kNegInf;
         if (owned<DT>(e.place[i], first, step)) {
-            const int s = rank_of(g, t.id[i]), at = t.id[i] - g.col0[s];
-            z[i] = load1<DT>(row_of<DT>(g, s, row), at);
-            out[i] = grad_row_of<DT>(g, s, row) + (long long)at * elem_bytes<DT>();
+            z[i] = logit_at<DT>(g, row, t.id[i]);
+            out[i] = column_at<DT, true>(g, row, t.id[i]);
         }
     }
     merge_repeats<DT>(e, t, first, step, q);
@@ -260,13 +259,8 @@ __device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const Dis
     }
     stream.run(g, row, step, lane, [&](const TileWalk &w, int u, int e0, int held, u32x4 raw) {
         Pack<DT> v = unpack<DT>(raw);
-        if (ref.wide) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) v.v[i] = (v.v[i] - ref.m) * g.c;
-        } else {
-#pragma unroll
-            for (int i = 0; i < K; ++i) v.v[i] = __builtin_fmaf(v.v[i], g.c, -ref.y);
-        }
+        for (int i = 0; i < K; ++i) v.v[i] = rel(v.v[i], ref);
 #pragma unroll
         for (int i = 0; i < K; ++i) v.v[i] = exp2_fast(v.v[i] - r2) * cu;
         store_vec<DT>(grad_row_of<DT>(g, w.s, row), v, w.j, e0, held, w.w);
@@ -277,7 +271,7 @@ __device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const Dis
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (owned<DT>(e.place[i], first, step))
-            store1<DT>(out[i], 0, round_to<DT>((t.total * exp2_fast(rel(z[i], ref, g.c) - lse2) - q[i]) * gs));
+            store1<DT>(out[i], 0, round_to<DT>((t.total * exp2_fast(rel(z[i], ref) - lse2) - q[i]) * gs));
     }
 }
 
@@ -314,7 +308,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
         for (int i = 0; i < PER; ++i) li.m = __builtin_fmaxf(li.m, e.z[i]);
         const Ref ref = make_ref(li.m, g.c);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) li.s += exp2_fast(rel(e.z[i], ref, g.c));
+        for (int i = 0; i < PER; ++i) li.s += exp2_fast(rel(e.z[i], ref));
         block_stats<false>(li, lds_listed, waves, wave, lane, g.c);
     }
     if (g.parts > 1) {

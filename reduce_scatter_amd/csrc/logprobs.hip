@@ -36,7 +36,7 @@ template <int NR>
 __device__ __forceinline__ void write_row(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row, const Stats &st,
                                           const RowResult &res, float xt, bool token) {
     const Ref ref = make_ref(st.m, g.c);
-    if (a.logprobs) a.logprobs[row] = !token ? 0.0f : res.empty ? kNegInf : rel_ln(xt, ref, g.c, g.inv_t) - res.lse;
+    if (a.logprobs) a.logprobs[row] = !token ? 0.0f : res.empty ? kNegInf : rel_ln(xt, ref, g.inv_t) - res.lse;
     if (a.entropy) a.entropy[row] = res.entropy;
     if (a.saved) {
         float *o = a.saved + row * 4;
@@ -53,7 +53,7 @@ __device__ __forceinline__ void write_top(const VocabGeom<NR> &g, const Logprobs
     const Ref ref = make_ref(st.m, g.c);
     const float x = order_value((uint32_t)(key >> 32));
     a.top_ids[row * a.k + i] = key ? (int64_t)key_col(key) : -1;
-    a.top_logprobs[row * a.k + i] = !key || res.empty ? kNegInf : rel_ln(x, ref, g.c, g.inv_t) - res.lse;
+    a.top_logprobs[row * a.k + i] = !key || res.empty ? kNegInf : rel_ln(x, ref, g.inv_t) - res.lse;
 }
 
 // f(keys) with those keys (0: none) that are not below `least` among the
@@ -67,7 +67,8 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
     const float floor = order_value((uint32_t)(least >> 32));
     const int half = lane >> 5, tile = (lane & 31) / kVocabU, u = lane % kVocabU;
     for (int base = first; base < g.tiles; base += 8 * step) {
-        int t = base + tile * step, s = 0, before = 0, tiles = 0;
+        const int t = base + tile * step;
+        int s = 0, before = 0, tiles = 0;
         each_later_rank(g, [&](int r) {
             tiles += tiles_of<DT>(g, r - 1);
             s = t >= tiles ? r : s;
@@ -75,14 +76,15 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
         });
         const bool there = t < g.tiles;
         s = there ? s : 0;
-        const int w = there ? width_of<DT>(g, s) : 0, col = g.col0[s];
+        const int w = there ? width_of<DT>(g, s) : 0, col = g.col0[s], j = t - before;
         const char *x = row_of<DT>(g, s, row);
-        const int j = t - before;
         for (u64 pending = lanes; pending;) {
             u32x4 v[kAhead];
             int e0[kAhead];
+            const int loads = (__builtin_popcountll(pending) + 1) / 2;
 #pragma unroll
             for (int b = 0; b < kAhead; ++b) {
+                if (b >= loads) break;
                 const int one = pending ? __builtin_ctzll(pending) : -1;
                 pending &= pending - 1;
                 const int two = pending ? __builtin_ctzll(pending) : -1;
@@ -105,6 +107,7 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
             }
 #pragma unroll
             for (int b = 0; b < kAhead; ++b) {
+                if (b >= loads) break;
                 const Pack<DT> z = unpack<DT>(v[b]);
                 const int held = held0<DT, kTiny<NR>>(e0[b], w);
 #pragma unroll
@@ -194,13 +197,8 @@ __device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const Log
     stream.start(g, row, first, lane);
     stream.run(g, row, step, lane, [&](const TileWalk &t, int u, int e0, int held, u32x4 raw) {
         Pack<DT> x = unpack<DT>(raw);
-        if (ref.wide) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) x.v[i] = (x.v[i] - ref.m) * g.c;
-        } else {
-#pragma unroll
-            for (int i = 0; i < K; ++i) x.v[i] = __builtin_fmaf(x.v[i], g.c, -ref.y);
-        }
+        for (int i = 0; i < K; ++i) x.v[i] = rel(x.v[i], ref);
         if (gh == 0.0f) {
 #pragma unroll
             for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * a0;

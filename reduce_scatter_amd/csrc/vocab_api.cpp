@@ -63,9 +63,14 @@ ar_status_t check_shape(const ar_vocab_t *v, Shape &s) {
     // 2, 4, 8 waves: 330, 336, 346, 375; on 777 x 50021: 168, 114, 94, 97.
     int waves = 1;
     while (waves < kVocabWaves && waves * 2 <= tiles && v->rows * waves < 16384) waves *= 2;
-    // Workgroups per row, while the rows alone leave compute units idle.
+    // Workgroups per row, while the rows alone leave compute units idle and
+    // every wave keeps two tiles; joining them is a second launch (about 4 us),
+    // so not below five tiles a wave: 64 x 131072 bf16 with 20 alternatives
+    // (us) in 1, 2, 4, 8 workgroups: 22.5, 22.1, 19.1, 22.9; one row of 32768: 11.0,
+    // 13.7, 13.7, 13.6; a distillation step on 16 x 32768 fp32: 13.3, 17.9, 16.9, 16.7.
     int parts = 1;
-    while (parts < kVocabParts && parts * 2 * waves <= tiles && v->rows * parts * 2 <= 256) parts *= 2;
+    while (tiles > 4 * waves && parts < kVocabParts && parts * 4 * waves <= tiles && v->rows * parts * 2 <= 256)
+        parts *= 2;
     s.c.waves = waves;
     s.c.parts = parts;
     return AR_OK;

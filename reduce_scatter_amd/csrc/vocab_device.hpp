@@ -30,27 +30,28 @@ constexpr float kTLow = -1e6f;         // stands for lower t (2^t = 0 far above 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_huge_valf(); }
 
-// The reference of a set of logits.  y stands for m*c; m = -inf (nothing but
-// masked logits so far) counts from 0.  Where m is so large that m*c
-// overflows, t is computed from x - m instead (`wide`).
+// The reference of a set of logits: t = x*c - y.  m = -inf (nothing but masked
+// logits) counts from 0.  Where m is so large that m*c overflows (a row of the
+// lowest value, say), c is 1 and t = x - m: any other number is then at least
+// 2^104 away, so 2^t is 1 or 0 under either scale.
 struct Ref {
-    float m, y;
-    bool wide;
+    float m, y, c;
+    bool wide;                         // c is 1 instead of log2(e) / T
 };
 __device__ __forceinline__ Ref make_ref(float m, float c) {
     Ref r;
     r.m = m;
     r.y = m == kNegInf ? 0.0f : m * c;
     r.wide = finite(m) && !finite(r.y);
+    r.y = r.wide ? m : r.y;
+    r.c = r.wide ? 1.0f : c;
     return r;
 }
-__device__ __forceinline__ float rel(float x, const Ref &r, float c) {
-    return r.wide ? (x - r.m) * c : __builtin_fmaf(x, c, -r.y);
-}
-// (x - m) / T in natural units, also where the larger number in units of log2 overflows.
-__device__ __forceinline__ float rel_ln(float x, const Ref &r, float c, float inv_t) {
-    const float t = rel(x, r, c);
-    return finite(t) ? kLn2 * t : (x - r.m) * inv_t;
+__device__ __forceinline__ float rel(float x, const Ref &r) { return __builtin_fmaf(x, r.c, -r.y); }
+// (x - m) / T in natural units, also where t overflows or has the other scale.
+__device__ __forceinline__ float rel_ln(float x, const Ref &r, float inv_t) {
+    const float t = rel(x, r);
+    return finite(t) && !r.wide ? kLn2 * t : (x - r.m) * inv_t;
 }
 // log2 of the factor that takes sums relative to `from` to reference `to` (to.m >= from.m).
 __device__ __forceinline__ float ref_shift(const Ref &from, const Ref &to, float c) {
@@ -336,9 +337,15 @@ template <int NR> __device__ __forceinline__ int rank_of(const VocabGeom<NR> &g,
     each_later_rank(g, [&](int r) { s += id >= g.col0[r]; });
     return s;
 }
-template <int DT, int NR> __device__ __forceinline__ float logit_at(const VocabGeom<NR> &g, long long row, int id) {
+// Where column id's logit (GRAD: gradient) of the row lies.
+template <int DT, bool GRAD, int NR>
+__device__ __forceinline__ char *column_at(const VocabGeom<NR> &g, long long row, int id) {
     const int s = rank_of(g, id);
-    return load1<DT>(row_of<DT>(g, s, row), id - g.col0[s]);
+    return (GRAD ? grad_row_of<DT>(g, s, row) : const_cast<char *>(row_of<DT>(g, s, row))) +
+           (uint32_t)(id - g.col0[s]) * elem_bytes<DT>();
+}
+template <int DT, int NR> __device__ __forceinline__ float logit_at(const VocabGeom<NR> &g, long long row, int id) {
+    return load1<DT>(column_at<DT, false>(g, row, id), 0);
 }
 
 // Column id's tile and its element there, counted from the tile's first.
@@ -359,8 +366,8 @@ template <int DT, int NR> __device__ __forceinline__ Place place_of(const VocabG
 // A lane's running sums and reference.
 struct Running {
     Stats st{kNegInf, 0.0f, 0.0f};
-    Ref ref{kNegInf, 0.0f, false};
-    int slow = 1;                      // some lane has met no logit above -inf yet, or its reference is wide
+    Ref ref{kNegInf, 0.0f, 1.0f, false};
+    int fresh = 1;                     // some lane has met no logit above -inf yet
 };
 // max(t, kTLow) as one instruction: the builtin first quiets a signalling
 // NaN, which no result of arithmetic is.
@@ -369,22 +376,20 @@ __device__ __forceinline__ float hold_up(float t) {
     asm("v_max_f32 %0, %1, %2" : "=v"(r) : "s"(kTLow), "v"(t));
     return r;
 }
-// Add one vector's logits to a lane's sums (SLOW: any reference).  2^t = 0
-// where t = -inf, but 0 * -inf is NaN: t is held above kTLow in the weighted
+// Add one vector's logits to a lane's sums.  2^t = 0 where t = -inf, but 0 * -inf is NaN: t is held above kTLow in the weighted
 // sum.
-template <int DT, bool S1, bool SLOW> __device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v, float c) {
+template <int DT, bool S1> __device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v) {
 #pragma unroll
     for (int i = 0; i < Lanes<DT>::value; ++i) {
-        const float t = SLOW ? rel(v.v[i], a.ref, c) : __builtin_fmaf(v.v[i], c, -a.ref.y);
-        const float e = exp2_fast(t);
+        const float t = rel(v.v[i], a.ref), e = exp2_fast(t);
         a.st.s += e;
         if constexpr (S1) a.st.s1 = __builtin_fmaf(e, hold_up(t), a.st.s1);
     }
 }
 template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, float c) {
     const Stats before = a.st;
-    add_terms<DT, S1, false>(a, x, c);
-    if (__ballot(a.st.s > 65536.0f) | (u64)a.slow) {                 // the first vector, and seldom again: add it with care
+    add_terms<DT, S1>(a, x);
+    if (__ballot(a.st.s > 65536.0f) | (u64)a.fresh) {                 // the first vector, and seldom again: add it with care
         a.st = before;
         Pack<DT> v = x;
         // other values to the compiler, which would otherwise take the first steps below for every vector
@@ -397,8 +402,8 @@ template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, c
             shift_stats(a.st, m, c);
             a.ref = make_ref(m, c);
         }
-        a.slow = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf || a.ref.wide));
-        add_terms<DT, S1, true>(a, v, c);
+        a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
+        add_terms<DT, S1>(a, v);
     }
 }
 

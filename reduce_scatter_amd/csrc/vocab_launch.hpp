@@ -23,6 +23,7 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
         col += (int)c.widths[r];
     }
     for (int r = c.n; r <= NR; ++r) g.col0[r] = col;           // no column is past them
+    for (int r = c.n; r < NR; ++r) g.x[r] = nullptr, g.g[r] = nullptr, g.pitch[r] = g.gpitch[r] = 0;
     g.n = c.n;
     g.parts = c.parts;
     g.tiles = c.tiles;
