@@ -78,6 +78,7 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
         s = there ? s : 0;
         const int w = there ? width_of<DT>(g, s) : 0, col = g.col0[s], j = t - before;
         const char *x = row_of<DT>(g, s, row);
+        const int phase = phase_of<DT, kTiny<NR>>(x, w);
         for (u64 pending = lanes; pending;) {
             u32x4 v[kAhead];
             int e0[kAhead];
@@ -90,9 +91,9 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
                 const int two = pending ? __builtin_ctzll(pending) : -1;
                 pending &= pending - 1;
                 const int from = half ? two : one;
-                e0[b] = elem0<DT>(j, u, from);
-                if (from < 0 || e0[b] >= w) {
-                    e0[b] = -1;
+                e0[b] = ((j * kVocabU + u) * 64 + from) * K - phase;
+                if (!there || from < 0 || e0[b] >= w) {
+                    e0[b] = w;
                 } else if (kTiny<NR> && w < K) {
                     v[b] = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -112,9 +113,9 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
                 const int held = held0<DT, kTiny<NR>>(e0[b], w);
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
-                    if (!__any(e0[b] >= 0 && !(z.v[i] < floor))) continue;
+                    if (!__any(e0[b] < w && !(z.v[i] < floor))) continue;
                     u64 key = top_key(z.v[i], col + held + i);
-                    if (e0[b] < 0 || held + i < e0[b] || held + i >= w || key < least) key = 0;
+                    if (e0[b] >= w || held + i < e0[b] || held + i >= e0[b] + K || held + i >= w || key < least) key = 0;
                     if (__any(key != 0)) f(key);
                 }
             }
@@ -175,44 +176,61 @@ __device__ __forceinline__ void select_top(const VocabGeom<NR> &g, long long row
     if (thread < k) emit(thread, v);
 }
 
-// Gradient of this workgroup's tiles: with e = 2^t and p = e / S,
+// Gradient of a row: with e = 2^t and p = e / S,
 //   dx = [v = target] gl/T + e * (a0 + a1 t),
 //   a0 = -(gl + gh (H - ln S)) / (T S),  a1 = -gh ln2 / (T S).
+struct RowGradient {
+    Ref ref;
+    float a0, a1, at_target;
+    Place p;                           // of the target
+    bool zero;
+};
 template <int DT, int NR>
-__device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row,
-                                               const Stats &st, const RowResult &res, int target, int first, int step,
-                                               int lane) {
-    constexpr int K = Lanes<DT>::value;
+__device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, const LogprobsArgs &a, long long row,
+                                                    const Stats &st, const RowResult &res, int target) {
     const float gl = a.grad_logprobs && target >= 0 ? a.grad_logprobs[row] : 0.0f;
     const float gh = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
-    const float a0 = -(gl + gh * (res.entropy - res.lse)) * g.inv_t / st.s;
-    const float a1 = -gh * kLn2 * g.inv_t / st.s;
-    const Ref ref = make_ref(st.m, g.c);
-    const Place p = target >= 0 ? place_of<DT>(g, target) : Place{-1, 0};
-    if (res.empty || (gl == 0.0f && gh == 0.0f)) {
+    RowGradient r;
+    r.ref = make_ref(st.m, g.c);
+    r.a0 = -(gl + gh * (res.entropy - res.lse)) * g.inv_t / st.s;
+    r.a1 = -gh * kLn2 * g.inv_t / st.s;
+    r.at_target = gl * g.inv_t;
+    r.p = target >= 0 ? place_of<DT>(g, row, target) : Place{0, 0, -1, 0};
+    r.zero = res.empty || (gl == 0.0f && gh == 0.0f);
+    return r;
+}
+template <int DT, int NR>
+__device__ __forceinline__ void gradient_vec(const VocabGeom<NR> &g, const RowGradient &r, long long row,
+                                             const TileWalk &t, int e0, int held, u32x4 raw) {
+    constexpr int K = Lanes<DT>::value;
+    Pack<DT> x = unpack<DT>(raw);
+#pragma unroll
+    for (int i = 0; i < K; ++i) x.v[i] = rel(x.v[i], r.ref);
+    if (r.a1 == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * r.a0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * __builtin_fmaf(hold_up(x.v[i]), r.a1, r.a0);
+    }
+    if (t.at == r.p.t) {
+        const int d = t.j * kTileElems<DT> + r.p.et - t.phase - held;
+#pragma unroll
+        for (int i = 0; i < K; ++i) x.v[i] += i == d ? r.at_target : 0.0f;
+    }
+    store_vec<DT>(grad_row_of<DT>(g, t.s, row), x, t, e0, held);
+}
+template <int DT, int NR>
+__device__ __forceinline__ void gradient_tiles(const VocabGeom<NR> &g, const RowGradient &r, long long row, int first,
+                                               int step, int lane) {
+    if (r.zero) {
         zero_tiles<DT>(g, row, first, step, lane);
         return;
     }
     VectorStream<DT, true, NR> stream;
     stream.start(g, row, first, lane);
-    stream.run(g, row, step, lane, [&](const TileWalk &t, int u, int e0, int held, u32x4 raw) {
-        Pack<DT> x = unpack<DT>(raw);
-#pragma unroll
-        for (int i = 0; i < K; ++i) x.v[i] = rel(x.v[i], ref);
-        if (gh == 0.0f) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * a0;
-        } else {
-#pragma unroll
-            for (int i = 0; i < K; ++i)
-                x.v[i] = exp2_fast(x.v[i]) * __builtin_fmaf(hold_up(x.v[i]), a1, a0);
-        }
-        if (t.at == p.t) {
-            const int d = t.j * kTileElems<DT> + p.e - held;
-#pragma unroll
-            for (int i = 0; i < K; ++i) x.v[i] += i == d ? gl * g.inv_t : 0.0f;
-        }
-        store_vec<DT>(grad_row_of<DT>(g, t.s, row), x, t.j, e0, held, t.w);
+    stream.run(g, row, step, lane, [&](const TileWalk &t, int, int e0, int held, u32x4 raw) {
+        gradient_vec<DT>(g, r, row, t, e0, held, raw);
     });
 }
 
@@ -240,7 +258,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
     float best = kNegInf;
     int best_col = -1;
     stream.run(g, row, step, lane, [&](const TileWalk &t, int u, int e0, int held, u32x4 raw) {
-        if (!full_tile<DT>(t.j, t.w)) mask_vec<DT>(raw, e0, held, t.w);
+        if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
         const Pack<DT> v = unpack<DT>(raw);
         if constexpr (TOP) {
             float m = kNegInf;                                                     // NaN: ordered as -inf
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
             for (int i = 0; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
             if (e0 < t.w && (m > best || best_col < 0)) {
                 best = m;
-                best_col = t.col + e0;
+                best_col = t.col + max(e0, 0);
             }
         }
         add_vec<DT, S1>(run, v, g.c);
@@ -270,7 +288,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
             else write_top(g, a, row, st, res, key, i);
         });
     }
-    if constexpr (BOTH) gradient_tiles<DT>(g, a, row, st, res, target, first, step, lane);
+    if constexpr (BOTH) gradient_tiles<DT>(g, row_gradient<DT>(g, a, row, st, res, target), row, first, step, lane);
 }
 
 // A row's results from its parts: one lane per part for the statistics, one
@@ -315,13 +333,45 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_backward_kernel(con
     res.empty = st.m == kNegInf && st.s == 0.0f;
     res.lse = logf(st.s);
     res.entropy = o[2];
-    gradient_tiles<DT>(g, a, row, st, res, token_of(a, row, g.col0[g.n]), part * waves + wave, waves * g.parts, lane);
+    const RowGradient r = row_gradient<DT>(g, a, row, st, res, token_of(a, row, g.col0[g.n]));
+    gradient_tiles<DT>(g, r, row, part * waves + wave, waves * g.parts, lane);
+}
+
+// Results and gradient of a row held in the workgroup's registers.
+template <int DT, int NR, bool S1, int T>
+__global__ __launch_bounds__(64 * kHeldWaves) void logprobs_held_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
+    __shared__ Stats lds_stats[kHeldWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int waves = blockDim.x >> 6;
+    const long long row = g.row0 + blockIdx.x;
+    HeldTiles<DT, NR, T> tiles;
+    tiles.start(g, row, wave, waves, lane);
+    const int target = token_of(a, row, g.col0[g.n]);
+    const float xt = wave == 0 && target >= 0 ? logit_at<DT>(g, row, target) : 0.0f;
+    Stats st = held_sums<DT, S1>(g, tiles, lane, [](int, int, int, int, u32x4 &) {});
+    block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
+    const RowResult res = row_result(st);
+    if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
+    const RowGradient r = row_gradient<DT>(g, a, row, st, res, target);
+    if (r.zero) {
+        zero_tiles<DT>(g, row, wave, waves, lane);
+        return;
+    }
+    tiles.each(lane, [&](const TileWalk &t, int, int, int e0, int held, u32x4 raw) {
+        gradient_vec<DT>(g, r, row, t, e0, held, raw);
+    });
 }
 
 template <int DT, int NR>
 hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage stage, hipStream_t s) {
     const bool s1 = a.entropy || a.saved || a.grad_entropy, top = a.k > 0;
     if (stage == kBackward) return launch_rows<NR>(c, a, logprobs_backward_kernel<DT, NR>, c.parts, c.waves, s);
+    if (stage == kBoth && c.held == 1)
+        return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, 1>, 1, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, 1>, 1, c.waves, s);
+    if (stage == kBoth && c.held)
+        return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, kHeldTiles>, 1, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, kHeldTiles>, 1, c.waves, s);
     if (stage == kBoth) {
         return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true>, 1, c.waves, s)
                   : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true>, 1, c.waves, s);

@@ -87,6 +87,17 @@ VocabCall short_rows(const Shape &s) {
     return c;
 }
 
+// Results and gradient in one launch: the row stays in registers where it
+// fits into 16 waves of four tiles (131072 columns of 16-bit logits, half that
+// in fp32).
+// Lists of more than 64 entries take the registers themselves.
+VocabCall both_rows(const Shape &s, int listed) {
+    VocabCall c = s.c;
+    c.held = c.rows <= 256 && c.tiles <= kHeldWaves ? 1 : kHeldTiles;
+    c.waves = (c.tiles + c.held - 1) / c.held;
+    return c;
+}
+
 // Workspace: partial statistics, partial lists, statistics for a gradient
 // that follows in a second launch.  Nothing where a row is one workgroup's.
 struct Space {
@@ -106,6 +117,18 @@ ar_status_t check_space(const Space &w, const void *workspace, size_t bytes) {
     if (w.bytes == 0) return AR_OK;
     if (!workspace || bytes < w.bytes) return AR_ERR_INVALID_ARG;
     return (uintptr_t)workspace % 16 ? AR_ERR_ALIGNMENT : AR_OK;
+}
+
+// The row's tiles lie on 16-byte boundaries of memory, so rows off them may
+// reach into one tile more.
+void set_logits(Shape &s, const void *const *x) {
+    const int e = s.c.dtype == AR_FLOAT32 ? 4 : 2, lanes = 16 / e, tile = 64 * kVocabU * lanes;
+    s.c.x = x;
+    for (int r = 0; r < s.c.n; ++r)
+        if (s.c.widths[r] && ((uintptr_t)x[r] % 16 || (s.c.rows > 1 && s.c.pitches[r] * e % 16))) s.c.skew = lanes - 1;
+    s.c.tiles = 0;
+    for (int r = 0; r < s.c.n; ++r)
+        if (s.c.widths[r]) s.c.tiles += (int)((s.c.widths[r] + s.c.skew + tile - 1) / tile);
 }
 
 // One rank's buffer: present where it has columns, aligned to its elements.
@@ -207,7 +230,7 @@ ar_status_t ar_logprobs(const void *const *logits, const ar_vocab_t *shape, cons
         return AR_ERR_ALIGNMENT;
     const Space w = space_of(s, top_k);
     if ((st = check_space(w, workspace, workspace_bytes)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     LogprobsArgs a{};
     a.targets = targets;
     a.logprobs = logprobs;
@@ -238,7 +261,7 @@ ar_status_t ar_logprobs_backward(const void *const *logits, void *const *grads, 
     if (misaligned(targets, 8) || misaligned(saved, 4) || misaligned(grad_logprobs, 4) || misaligned(grad_entropy, 4))
         return AR_ERR_ALIGNMENT;
     if ((st = check_grads(s, logits, grads)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     s.c.g = grads;
     LogprobsArgs a{};
     a.targets = targets;
@@ -265,7 +288,7 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
     if ((st = check_grads(s, logits, grads)) != AR_OK) return st;
     const Space w = space_of(s, 0);
     if ((st = check_space(w, workspace, workspace_bytes)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     s.c.g = grads;
     LogprobsArgs a{};
     a.targets = targets;
@@ -274,7 +297,7 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
     a.saved = saved;
     a.grad_logprobs = grad_logprobs;
     a.grad_entropy = grad_entropy;
-    if (s.c.parts == 1) return hip_status(launch_logprobs(short_rows(s), a, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_logprobs(both_rows(s, 0), a, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_logprobs(s.c, a, kForward, stream);
@@ -296,7 +319,7 @@ ar_status_t ar_distill(const void *const *logits, const ar_vocab_t *shape, const
     if (misaligned(loss, 4) || misaligned(saved, 4)) return AR_ERR_ALIGNMENT;
     const Space w = space_of(s, 0);
     if ((st = check_space(w, workspace, workspace_bytes)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     DistillArgs a{};
     a.ids = teacher_ids;
     a.values = teacher_values;
@@ -323,7 +346,7 @@ ar_status_t ar_distill_backward(const void *const *logits, void *const *grads, c
         return st;
     if (misaligned(saved, 4) || misaligned(grad_loss, 4)) return AR_ERR_ALIGNMENT;
     if ((st = check_grads(s, logits, grads)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     s.c.g = grads;
     DistillArgs a{};
     a.ids = teacher_ids;
@@ -349,7 +372,7 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     if ((st = check_grads(s, logits, grads)) != AR_OK) return st;
     const Space w = space_of(s, 0);
     if ((st = check_space(w, workspace, workspace_bytes)) != AR_OK) return st;
-    s.c.x = logits;
+    set_logits(s, logits);
     s.c.g = grads;
     DistillArgs a{};
     a.ids = teacher_ids;
@@ -359,7 +382,7 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     a.saved = saved;
     a.grad_loss = grad_loss;
     const bool tail = mode == AR_TEACHER_TAIL;
-    if (s.c.parts == 1) return hip_status(launch_distill(short_rows(s), a, tail, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s, k), a, tail, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_distill(s.c, a, tail, kForward, stream);

@@ -138,7 +138,8 @@ template <int DT, int NR> __device__ __forceinline__ int width_of(const VocabGeo
     return g.col0[s + 1] - g.col0[s];
 }
 template <int DT, int NR> __device__ __forceinline__ int tiles_of(const VocabGeom<NR> &g, int s) {
-    return (width_of<DT>(g, s) + kTileElems<DT> - 1) / kTileElems<DT>;
+    const int w = width_of<DT>(g, s);
+    return w ? (w + g.skew + kTileElems<DT> - 1) / kTileElems<DT> : 0;
 }
 
 template <int DT, int NR> __device__ __forceinline__ const char *row_of(const VocabGeom<NR> &g, int s, long long row) {
@@ -148,11 +149,21 @@ template <int DT, int NR> __device__ __forceinline__ char *grad_row_of(const Voc
     return g.g[s] + row * (long long)g.gpitch[s] * elem_bytes<DT>();
 }
 
+template <int NR> constexpr bool kTiny = NR > kVocabFew;
+// Vectors lie on 16-byte boundaries of memory: a row that begins `phase`
+// elements after one has its first vector cut short.  (Ranks of fewer columns
+// than a vector, TINY, are read by the element.)
+template <int DT, bool TINY> __device__ __forceinline__ int phase_of(const char *x, int w) {
+    if (TINY && w < Lanes<DT>::value) return 0;
+    return (int)((uintptr_t)x / elem_bytes<DT>() % Lanes<DT>::value);
+}
+
 // A wave's way through its tiles: the tile (numbered over all ranks), its
 // rank, its number within the rank, and what the rank's tiles have in common.
 struct TileWalk {
     int at, s, j;
     int w, tiles, col;                 // the rank's width, tiles and first column
+    int phase;                         // elements from the 16-byte boundary below to the row's first
     const char *x;                     // its logits of the row
 
     // To the tile `by` further on; false past the last.
@@ -178,27 +189,29 @@ struct TileWalk {
         w = width_of<DT>(g, s);
         col = g.col0[s];
         x = row_of<DT>(g, s, row);
+        phase = phase_of<DT, kTiny<NR>>(x, w);
+    }
+    // First element (within the rank) of vector u of a lane: below 0 where the
+    // rank's first vector begins before the row does.
+    template <int DT> __device__ __forceinline__ int elem0(int u, int lane) const {
+        return ((j * kVocabU + u) * 64 + lane) * Lanes<DT>::value - phase;
+    }
+    template <int DT> __device__ __forceinline__ bool full() const {
+        return j * kTileElems<DT> >= phase && (j + 1) * kTileElems<DT> - phase <= w;
     }
 };
 
-// First element (within the rank) of vector u of this lane in tile j.
-template <int DT> __device__ __forceinline__ int elem0(int j, int u, int lane) {
-    return ((j * kVocabU + u) * 64 + lane) * Lanes<DT>::value;
-}
-template <int DT> __device__ __forceinline__ bool full_tile(int j, int w) { return (j + 1) * kTileElems<DT> <= w; }
-
-// Where register element 0 of that vector stands.  The vector covers elements
-// [e0, min(e0 + K, w)); past the last whole vector its registers hold the
-// rank's last K elements, of which those before e0 are another vector's, so
+// Where register element 0 of that vector stands.  The vector covers those of
+// [e0, e0 + K) that the rank has; where that is not all, its registers hold
+// the rank's first or last K elements, of which some are another vector's, so
 // that one unconditional in-bounds 16-byte load serves every lane of a rank of
 // at least K columns.  Ranks of fewer (TINY) are served by the kernels with
 // the large pointer table alone.
 template <int DT, bool TINY> __device__ __forceinline__ int held0(int e0, int w) {
     constexpr int K = Lanes<DT>::value;
     if (TINY && w < K) return e0;
-    return e0 < w - K ? e0 : w - K;
+    return min(max(e0, 0), w - K);
 }
-template <int NR> constexpr bool kTiny = NR > kVocabFew;
 
 template <int DT> __device__ __forceinline__ uint32_t neg_inf_bits() {
     return DT == F32 ? 0xff800000u : DT == BF16 ? 0xff80u : 0xfc00u;
@@ -221,18 +234,17 @@ __device__ __forceinline__ u32x4 load_vec(const TileWalk &t, int u, int lane) {
         }
     }
     // in bytes, from the lane's part and the wave's, so that two instructions make the address
-    const uint32_t at = (uint32_t)lane * 16u + (uint32_t)elem0<DT>(t.j, u, 0) * elem_bytes<DT>();
-    const uint32_t last = (uint32_t)(t.w - K) * elem_bytes<DT>();
-    const u32x4e *p = (const u32x4e *)(t.x + (at < last ? at : last));
+    const int at = lane * 16 + t.elem0<DT>(u, 0) * elem_bytes<DT>();
+    const u32x4e *p = (const u32x4e *)(t.x + (uint32_t)min(max(at, 0), (t.w - K) * elem_bytes<DT>()));
     if constexpr (STREAM) return __builtin_nontemporal_load(p);
     else return *p;
 }
-// Registers of a vector at a rank's end that hold no element of it become -inf.
+// Registers of a vector at a rank's ends that hold no element of it become -inf.
 template <int DT> __device__ __forceinline__ void mask_vec(u32x4 &v, int e0, int held, int w) {
     constexpr int K = Lanes<DT>::value;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const bool out = held + i < e0 || held + i >= w;
+        const bool out = held + i < e0 || held + i >= e0 + K || held + i >= w;
         if constexpr (DT == F32) v[i] = out ? neg_inf_bits<DT>() : v[i];
         else {
             const uint32_t part = 0xffffu << (i & 1) * 16, ninf = neg_inf_bits<DT>() << (i & 1) * 16;
@@ -267,7 +279,7 @@ template <int DT, bool STREAM, int NR> struct VectorStream {
             if (!more) n = t;
 #pragma unroll
             for (int u = 0; u < kVocabU; ++u) {
-                const int e0 = elem0<DT>(t.j, u, lane);
+                const int e0 = t.elem0<DT>(u, lane);
                 f(t, u, e0, held0<DT, TINY>(e0, t.w), v[u]);
                 v[u] = load_vec<DT, STREAM, TINY>(n, u, lane);
             }
@@ -293,16 +305,16 @@ template <int DT> __device__ __forceinline__ u32x4 round_pack(const Pack<DT> &p)
     return w;
 }
 // Store a vector whose register 0 stands at element `held`: whole, or at a
-// rank's end only the elements from e0 on (the others are another vector's).
+// rank's ends only the elements that are its own.
 template <int DT>
-__device__ __forceinline__ void store_vec(char *g, const Pack<DT> &p, int j, int e0, int held, int w) {
+__device__ __forceinline__ void store_vec(char *g, const Pack<DT> &p, const TileWalk &t, int e0, int held) {
     constexpr int K = Lanes<DT>::value;
-    if (full_tile<DT>(j, w) || e0 + K <= w) {
+    if (t.full<DT>() || (e0 >= 0 && e0 + K <= t.w)) {
         __builtin_nontemporal_store(round_pack<DT>(p), (u32x4e *)(g + (uint32_t)e0 * elem_bytes<DT>()));
     } else {
 #pragma unroll
         for (int i = 0; i < K; ++i)
-            if (held + i >= e0 && held + i < w) store1<DT>(g, held + i, round_to<DT>(p.v[i]));
+            if (held + i >= e0 && held + i < e0 + K && held + i < t.w) store1<DT>(g, held + i, round_to<DT>(p.v[i]));
     }
 }
 
@@ -315,8 +327,8 @@ __device__ __forceinline__ void zero_tiles(const VocabGeom<NR> &g, long long row
     for (bool more = t.start<DT>(g, row, first); more; more = t.move<DT>(g, row, step)) {
 #pragma unroll
         for (int u = 0; u < kVocabU; ++u) {
-            const int e0 = elem0<DT>(t.j, u, lane);
-            store_vec<DT>(grad_row_of<DT>(g, t.s, row), zero, t.j, e0, held0<DT, kTiny<NR>>(e0, t.w), t.w);
+            const int e0 = t.elem0<DT>(u, lane);
+            store_vec<DT>(grad_row_of<DT>(g, t.s, row), zero, t, e0, held0<DT, kTiny<NR>>(e0, t.w));
         }
     }
 }
@@ -337,30 +349,26 @@ template <int NR> __device__ __forceinline__ int rank_of(const VocabGeom<NR> &g,
     each_later_rank(g, [&](int r) { s += id >= g.col0[r]; });
     return s;
 }
-// Where column id's logit (GRAD: gradient) of the row lies.
-template <int DT, bool GRAD, int NR>
-__device__ __forceinline__ char *column_at(const VocabGeom<NR> &g, long long row, int id) {
-    const int s = rank_of(g, id);
-    return (GRAD ? grad_row_of<DT>(g, s, row) : const_cast<char *>(row_of<DT>(g, s, row))) +
-           (uint32_t)(id - g.col0[s]) * elem_bytes<DT>();
-}
 template <int DT, int NR> __device__ __forceinline__ float logit_at(const VocabGeom<NR> &g, long long row, int id) {
-    return load1<DT>(column_at<DT, false>(g, row, id), 0);
+    const int s = rank_of(g, id);
+    return load1<DT>(row_of<DT>(g, s, row), id - g.col0[s]);
 }
 
-// Column id's tile and its element there, counted from the tile's first.
+// Column id's rank and its element there; its tile, and its element within that.
 struct Place {
-    int t, e;
+    int s, e, t, et;
 };
-template <int DT, int NR> __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, int id) {
-    int first = 0, t = 0;
+template <int DT, int NR>
+__device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, long long row, int id) {
+    int s = 0, first = 0, t = 0;
     each_later_rank(g, [&](int r) {
         const bool past = id >= g.col0[r];
+        s = past ? r : s;
         first = past ? g.col0[r] : first;
         t += past ? tiles_of<DT>(g, r - 1) : 0;
     });
-    const int e = id - first;
-    return {t + e / kTileElems<DT>, e % kTileElems<DT>};
+    const int e = id - first, at = e + phase_of<DT, kTiny<NR>>(row_of<DT>(g, s, row), width_of<DT>(g, s));
+    return {s, e, t + at / kTileElems<DT>, at % kTileElems<DT>};
 }
 
 // A lane's running sums and reference.
@@ -404,6 +412,86 @@ template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, c
         }
         a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
         add_terms<DT, S1>(a, v);
+    }
+}
+
+// ---- rows held in registers -------------------------------------------------
+// A wave's tiles, all of them (at most T): read once for sums and gradient
+// together.  Missing tiles are loaded as copies of the last one and never
+// used, so that the number of loads in flight is known (see VectorStream).
+template <int DT, int NR, int T> struct HeldTiles {
+    static constexpr bool TINY = kTiny<NR>;
+    TileWalk t[T];
+    int n;
+    u32x4 v[T * kVocabU];
+    __device__ __forceinline__ void start(const VocabGeom<NR> &g, long long row, int first, int step, int lane) {
+        t[0].template start<DT>(g, row, first);                        // a workgroup has no more waves than a row has tiles
+        n = 1;
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (k) {
+                t[k] = t[k - 1];
+                TileWalk next = t[k];
+                if (n == k && next.template move<DT>(g, row, step)) {
+                    t[k] = next;
+                    n = k + 1;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kVocabU; ++u) v[k * kVocabU + u] = load_vec<DT, true, TINY>(t[k], u, lane);
+        }
+    }
+    template <typename F> __device__ __forceinline__ void each(int lane, F f) {
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            if (k < n) {
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u) {
+                    // another number to the compiler, which would otherwise keep every vector's bounds from one
+                    // walk to the next, in more registers than there are
+                    int here = lane;
+                    asm volatile("" : "+v"(here));
+                    const int e0 = t[k].template elem0<DT>(u, here);
+                    f(t[k], k, u, e0, held0<DT, TINY>(e0, t[k].w), v[k * kVocabU + u]);
+                }
+            }
+        }
+    }
+};
+
+template <int DT> __device__ __forceinline__ float vec_max(const Pack<DT> &v) {
+    float m = v.v[0];
+#pragma unroll
+    for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
+    return m;
+}
+// Sums of a wave's held tiles, relative to one reference for the wave: the
+// maximum of its first vectors, unless a lane's sum shows it to be too low.
+// prepare(k, u, e0, held, raw) may change a vector before it is first used.
+template <int DT, bool S1, int NR, int T, typename F>
+__device__ __forceinline__ Stats held_sums(const VocabGeom<NR> &g, HeldTiles<DT, NR, T> &h, int lane, F prepare) {
+    Running a;
+    float m = kNegInf;
+    for (int pass = 0;; ++pass) {
+        h.each(lane, [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
+            asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));         // after the vector before: few values live
+            if (pass == 0) {
+                if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
+                prepare(k, u, e0, held, raw);
+            }
+            const Pack<DT> v = unpack<DT>(raw);
+            if (k == 0 && u == 0) {
+                if (pass == 0) m = wave_max(vec_max<DT>(v), lane);
+                a.st = Stats{m, 0.0f, 0.0f};
+                a.ref = make_ref(m, g.c);
+            }
+            add_terms<DT, S1>(a, v);
+        });
+        if (pass || !__any(a.st.s > 65536.0f || m == kNegInf)) return a.st;
+        h.each(lane, [&](const TileWalk &, int, int, int, int, u32x4 raw) {
+            m = __builtin_fmaxf(m, vec_max<DT>(unpack<DT>(raw)));
+        });
+        m = wave_max(m, lane);
     }
 }
 

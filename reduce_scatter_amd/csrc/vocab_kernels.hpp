@@ -16,6 +16,8 @@ namespace ar {
 
 constexpr int kVocabU = 4;             // 16-byte vectors per lane and tile
 constexpr int kVocabWaves = 8;         // most waves per workgroup
+constexpr int kHeldWaves = 16;         // the same for rows held in registers
+constexpr int kHeldTiles = 4;          // most tiles per wave of such a row (64 registers)
 constexpr int kVocabParts = 32;        // most workgroups per row
 constexpr int kVocabFew = 16;          // ranks of the small pointer table
 constexpr int kVocabMany = 128;        // ranks of the large one
@@ -29,6 +31,7 @@ template <int NR> struct VocabGeom {
     int col0[NR + 1];                  // first column of each rank; V from col0[n] on
     int n, parts;
     int tiles;                         // of the row, over all ranks
+    int skew;                          // 0, or where some row is off a 16-byte boundary a vector's elements less one
     float c;                           // log2(e) / T
     float inv_t;                       // 1 / T
     long long row0;                    // first row of this launch
@@ -59,6 +62,8 @@ struct VocabCall {
     int dtype;                         // ar::Dtype
     long long rows;
     int n, tiles, parts, waves;
+    int held;                          // kBoth: tiles per wave where a row fits in registers, 1 or kHeldTiles; 0: it does not
+    int skew;                          // as VocabGeom's
     bool tiny;                         // a rank has columns, but not enough for one vector
     const void *const *x;
     void *const *g;                    // nullptr for forward calls

@@ -27,6 +27,7 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
     g.n = c.n;
     g.parts = c.parts;
     g.tiles = c.tiles;
+    g.skew = c.skew;
     g.c = (float)(1.4426950408889634 / (double)c.temperature);
     g.inv_t = (float)(1.0 / (double)c.temperature);
 }
