@@ -106,16 +106,30 @@ __device__ __forceinline__ void each_key(const VocabGeom<NR> &g, long long row, 
                     v[b] = *(const u32x4e *)(x + (uint32_t)held0<DT, false>(e0[b], w) * elem_bytes<DT>());
                 }
             }
+            // one copy of what follows, and of f, which may be long
+#pragma unroll 1
+            for (int b = 0; b < loads && b < kAhead; ++b) {
+                u32x4 raw = v[0];
+                int from = e0[0];
 #pragma unroll
-            for (int b = 0; b < kAhead; ++b) {
-                if (b >= loads) break;
-                const Pack<DT> z = unpack<DT>(v[b]);
-                const int held = held0<DT, kTiny<NR>>(e0[b], w);
+                for (int i = 1; i < kAhead; ++i) {
+                    raw = b == i ? v[i] : raw;
+                    from = b == i ? e0[i] : from;
+                }
+                const Pack<DT> z = unpack<DT>(raw);
+                const int held = held0<DT, kTiny<NR>>(from, w);
+                uint32_t hits = 0;
 #pragma unroll
-                for (int i = 0; i < K; ++i) {
-                    if (!__any(e0[b] < w && !(z.v[i] < floor))) continue;
-                    u64 key = top_key(z.v[i], col + held + i);
-                    if (e0[b] >= w || held + i < e0[b] || held + i >= e0[b] + K || held + i >= w || key < least) key = 0;
+                for (int i = 0; i < K; ++i) hits |= z.v[i] < floor ? 0 : 1u << i;
+                hits = from < w ? hits : 0;
+                while (__any(hits != 0)) {
+                    const int i = __builtin_ctz(hits | 1u << K);
+                    float x = z.v[0];
+#pragma unroll
+                    for (int k = 1; k < K; ++k) x = i == k ? z.v[k] : x;
+                    u64 key = top_key(x, col + held + i);
+                    if (!hits || held + i < from || held + i >= from + K || held + i >= w || key < least) key = 0;
+                    hits &= hits - 1;
                     if (__any(key != 0)) f(key);
                 }
             }

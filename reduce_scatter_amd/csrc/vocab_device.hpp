@@ -459,40 +459,17 @@ template <int DT, int NR, int T> struct HeldTiles {
     }
 };
 
-template <int DT> __device__ __forceinline__ float vec_max(const Pack<DT> &v) {
-    float m = v.v[0];
-#pragma unroll
-    for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
-    return m;
-}
-// Sums of a wave's held tiles, relative to one reference for the wave: the
-// maximum of its first vectors, unless a lane's sum shows it to be too low.
-// prepare(k, u, e0, held, raw) may change a vector before it is first used.
+// Sums of a wave's held tiles; prepare(k, u, e0, held, raw) may change a vector before it is first used.
 template <int DT, bool S1, int NR, int T, typename F>
 __device__ __forceinline__ Stats held_sums(const VocabGeom<NR> &g, HeldTiles<DT, NR, T> &h, int lane, F prepare) {
     Running a;
-    float m = kNegInf;
-    for (int pass = 0;; ++pass) {
-        h.each(lane, [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
-            asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));         // after the vector before: few values live
-            if (pass == 0) {
-                if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
-                prepare(k, u, e0, held, raw);
-            }
-            const Pack<DT> v = unpack<DT>(raw);
-            if (k == 0 && u == 0) {
-                if (pass == 0) m = wave_max(vec_max<DT>(v), lane);
-                a.st = Stats{m, 0.0f, 0.0f};
-                a.ref = make_ref(m, g.c);
-            }
-            add_terms<DT, S1>(a, v);
-        });
-        if (pass || !__any(a.st.s > 65536.0f || m == kNegInf)) return a.st;
-        h.each(lane, [&](const TileWalk &, int, int, int, int, u32x4 raw) {
-            m = __builtin_fmaxf(m, vec_max<DT>(unpack<DT>(raw)));
-        });
-        m = wave_max(m, lane);
-    }
+    h.each(lane, [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
+        asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));     // after the vector before: few values live
+        if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
+        prepare(k, u, e0, held, raw);
+        add_vec<DT, S1>(a, unpack<DT>(raw), g.c);
+    });
+    return a.st;
 }
 
 // ---- top-k ----------------------------------------------------------------
