@@ -90,10 +90,10 @@ VocabCall short_rows(const Shape &s) {
 // Results and gradient in one launch: the row stays in registers where it
 // fits into 16 waves of four tiles (131072 columns of 16-bit logits, half that
 // in fp32) and those waves fill most of the 16 that a compute unit then holds.
-VocabCall both_rows(const Shape &s) {
+VocabCall both_rows(const Shape &s, int most) {
     VocabCall c = s.c;
     const int held = c.rows <= 256 && c.tiles <= kHeldWaves ? 1 : kHeldTiles, waves = (c.tiles + held - 1) / held;
-    if (waves > kHeldWaves || (c.rows > 256 && kHeldWaves / waves * waves < 14)) return short_rows(s);
+    if (waves > most || (c.rows > 256 && kHeldWaves / waves * waves < 14)) return short_rows(s);
     c.held = held;
     c.waves = waves;
     return c;
@@ -298,7 +298,7 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
     a.saved = saved;
     a.grad_logprobs = grad_logprobs;
     a.grad_entropy = grad_entropy;
-    if (s.c.parts == 1) return hip_status(launch_logprobs(both_rows(s), a, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_logprobs(both_rows(s, kHeldWaves), a, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_logprobs(s.c, a, kForward, stream);
@@ -383,7 +383,7 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     a.saved = saved;
     a.grad_loss = grad_loss;
     const bool tail = mode == AR_TEACHER_TAIL;
-    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s), a, tail, kBoth, stream));
+    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s, tail ? kHeldWaves / 2 : kHeldWaves), a, tail, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     hipError_t e = launch_distill(s.c, a, tail, kForward, stream);

@@ -394,24 +394,30 @@ template <int DT, bool S1> __device__ __forceinline__ void add_terms(Running &a,
         if constexpr (S1) a.st.s1 = __builtin_fmaf(e, hold_up(t), a.st.s1);
     }
 }
+// The same after moving the references of lanes whose vector has a larger maximum.
+template <int DT, bool S1> __device__ __forceinline__ void add_with_care(Running &a, Pack<DT> v, float c) {
+    // other values to the compiler, which would otherwise take the first steps below for every vector
+#pragma unroll
+    for (int i = 0; i < Lanes<DT>::value; ++i) asm volatile("" : "+v"(v.v[i]));
+    float m = v.v[0];
+#pragma unroll
+    for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
+    if (m > a.st.m) {
+        shift_stats(a.st, m, c);
+        a.ref = make_ref(m, c);
+    }
+    a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
+    add_terms<DT, S1>(a, v);
+}
+// Whether what has just been added has to be added again, with care: the
+// first vectors, and seldom later.
+__device__ __forceinline__ bool sums_off(const Running &a) { return (__ballot(a.st.s > 65536.0f) | (u64)a.fresh) != 0; }
 template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, float c) {
     const Stats before = a.st;
     add_terms<DT, S1>(a, x);
-    if (__ballot(a.st.s > 65536.0f) | (u64)a.fresh) {                 // the first vector, and seldom again: add it with care
+    if (sums_off(a)) {
         a.st = before;
-        Pack<DT> v = x;
-        // other values to the compiler, which would otherwise take the first steps below for every vector
-#pragma unroll
-        for (int i = 0; i < Lanes<DT>::value; ++i) asm volatile("" : "+v"(v.v[i]));
-        float m = v.v[0];
-#pragma unroll
-        for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
-        if (m > a.st.m) {
-            shift_stats(a.st, m, c);
-            a.ref = make_ref(m, c);
-        }
-        a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
-        add_terms<DT, S1>(a, v);
+        add_with_care<DT, S1>(a, x, c);
     }
 }
 
@@ -441,7 +447,8 @@ template <int DT, int NR, int T> struct HeldTiles {
             for (int u = 0; u < kVocabU; ++u) v[k * kVocabU + u] = load_vec<DT, true, TINY>(t[k], u, lane);
         }
     }
-    template <typename F> __device__ __forceinline__ void each(int lane, F f) {
+    // f for every vector, after(k) at the end of every tile
+    template <typename F, typename G> __device__ __forceinline__ void each(int lane, F f, G after) {
 #pragma unroll
         for (int k = 0; k < T; ++k) {
             if (k < n) {
@@ -454,8 +461,12 @@ template <int DT, int NR, int T> struct HeldTiles {
                     const int e0 = t[k].template elem0<DT>(u, here);
                     f(t[k], k, u, e0, held0<DT, TINY>(e0, t[k].w), v[k * kVocabU + u]);
                 }
+                after(k);
             }
         }
+    }
+    template <typename F> __device__ __forceinline__ void each(int lane, F f) {
+        each(lane, f, [](int) {});
     }
 };
 
@@ -463,12 +474,23 @@ template <int DT, int NR, int T> struct HeldTiles {
 template <int DT, bool S1, int NR, int T, typename F>
 __device__ __forceinline__ Stats held_sums(const VocabGeom<NR> &g, HeldTiles<DT, NR, T> &h, int lane, F prepare) {
     Running a;
-    h.each(lane, [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
-        asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));     // after the vector before: few values live
-        if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
-        prepare(k, u, e0, held, raw);
-        add_vec<DT, S1>(a, unpack<DT>(raw), g.c);
-    });
+    Stats before = a.st;                                       // at the tile's start
+    h.each(
+        lane,
+        [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
+            asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));         // after the vector before: few values live
+            if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
+            prepare(k, u, e0, held, raw);
+            add_terms<DT, S1>(a, unpack<DT>(raw));
+        },
+        [&](int k) {
+            if (sums_off(a)) {
+                a.st = before;
+#pragma unroll
+                for (int u = 0; u < kVocabU; ++u) add_with_care<DT, S1>(a, unpack<DT>(h.v[k * kVocabU + u]), g.c);
+            }
+            before = a.st;
+        });
     return a.st;
 }
 
