@@ -318,8 +318,9 @@ __device__ __forceinline__ void block_sums(Stats &st, Stats &li, SumScratch &lds
 }
 
 // Sums of a row (or of one part of it), the loss where the row is whole, and
-// with BOTH its gradient by the same workgroup.
-template <int DT, int NR, bool TAIL, bool BOTH>
+// with BOTH its gradient by the same workgroup.  AGAIN: the logits will be
+// read again soon and are left in the caches.
+template <int DT, int NR, bool TAIL, bool BOTH, bool AGAIN>
 __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGeom<NR> g, const DistillArgs a) {
     __shared__ SumScratch lds;
     __shared__ ListScratch list;
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
     const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
     const long long row = g.row0 + local;
     const int first = part * waves + wave;
-    VectorStream<DT, !BOTH, NR> stream;
+    VectorStream<DT, !AGAIN, NR> stream;
     stream.start(g, row, first, lane);
     const Teacher t = load_teacher<DT, TAIL>(g, a, list, row, lane);
     Running run;
@@ -440,11 +441,13 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_backward_kernel(cons
 template <int DT, int NR, bool TAIL>
 hipError_t run_distill(const VocabCall &c, const DistillArgs &a, VocabStage stage, hipStream_t s) {
     switch (stage) {
-    case kForward: return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false>, c.parts, c.waves, s);
+    case kForward:
+        if (c.again) return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, true>, c.parts, c.waves, s);
+        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, false>, c.parts, c.waves, s);
     case kBoth:
         if (c.held == 1) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 1>, 1, c.waves, s);
         if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s);
-        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true>, 1, c.waves, s);
+        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true, true>, 1, c.waves, s);
     case kBackward: return launch_rows<NR>(c, a, distill_backward_kernel<DT, NR, TAIL>, c.parts, c.waves, s);
     default: return launch_rows<NR>(c, a, distill_join_kernel<DT, NR, TAIL>, 1, 1, s);
     }

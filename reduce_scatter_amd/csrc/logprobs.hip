@@ -254,9 +254,9 @@ __device__ __forceinline__ int token_of(const LogprobsArgs &a, long long row, in
 }
 
 // Statistics of a row (or of one part of it), the results where the row is
-// whole, and with BOTH its gradient by the same workgroup, which finds the
-// row's logits in the caches.
-template <int DT, int NR, bool S1, bool TOP, bool BOTH>
+// whole, and with BOTH its gradient by the same workgroup.  AGAIN: the logits
+// will be read again soon and are left in the caches.
+template <int DT, int NR, bool S1, bool TOP, bool BOTH, bool AGAIN>
 __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabGeom<NR> g, const LogprobsArgs a) {
     __shared__ Stats lds_stats[kVocabWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
     const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
     const long long row = g.row0 + local;
     const int first = part * waves + wave;
-    VectorStream<DT, !BOTH, NR> stream;
+    VectorStream<DT, !AGAIN, NR> stream;
     stream.start(g, row, first, lane);
     const int target = token_of(a, row, g.col0[g.n]);
 
@@ -387,14 +387,15 @@ hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage st
         return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, kHeldTiles>, 1, c.waves, s)
                   : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, kHeldTiles>, 1, c.waves, s);
     if (stage == kBoth) {
-        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true>, 1, c.waves, s)
-                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true>, 1, c.waves, s);
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, true, true>, 1, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true, true>, 1, c.waves, s);
     }
     if (stage == kForward) {
-        if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false>, c.parts, c.waves, s)
-                           : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false>, c.parts, c.waves, s);
-        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false>, c.parts, c.waves, s)
-                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, false>, c.parts, c.waves, s);
+        if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false, false>, c.parts, c.waves, s)
+                           : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false, false>, c.parts, c.waves, s);
+        if (c.again) return launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false, true>, c.parts, c.waves, s);
+        return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false, false>, c.parts, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, false, false>, c.parts, c.waves, s);
     }
     int w = 1;
     while (top && w < c.parts && w < kVocabWaves) w *= 2;
