@@ -217,7 +217,7 @@ __device__ __forceinline__ void drop_listed(u32x4 &v, uint32_t bits, int u, int 
 struct RowGradient {
     Ref ref;
     float gs, total, lse2, r2, cu;
-    bool zero;
+    bool zero, shifted;
 };
 template <bool TAIL, int NR>
 __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, const DistillArgs &a, const Teacher &t,
@@ -235,14 +235,21 @@ __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, cons
         d.r2 = none ? 0.0f : r.tail2;
         d.cu = none ? 0.0f : (t.total * exp2_fast(r.tail2 - d.lse2) - t.qt) * d.gs;
     }
+    d.shifted = d.r2 < -60.0f;                                 // 2^-r2 does not fit into the factor
+    if (!d.shifted) d.cu *= exp2_fast(-d.r2);
     return d;
 }
 template <int DT, int NR>
 __device__ __forceinline__ void gradient_vec(const VocabGeom<NR> &g, const RowGradient &d, long long row,
                                              const TileWalk &w, int e0, int held, u32x4 raw) {
     Pack<DT> v = unpack<DT>(raw);
+    if (d.shifted) {
 #pragma unroll
-    for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = exp2_fast(rel(v.v[i], d.ref) - d.r2) * d.cu;
+        for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = exp2_fast(rel(v.v[i], d.ref) - d.r2) * d.cu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = term<DT>(v.v[i], d.ref, g).e * d.cu;
+    }
     store_vec<DT>(grad_row_of<DT>(g, w.s, row), v, w, e0, held);
 }
 // The listed columns among the workgroup's tiles; an id's entries all store
@@ -347,10 +354,11 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
                 if (u == 0) bits = tile_bits<DT>(places, a.k, w.at, lane);
                 drop_listed<DT>(raw, bits, u, e0, held);
             }
-            add_vec<DT, false>(run, unpack<DT>(raw), g.c);
+            if (u == 0) end_tile(run);
+            add_vec<DT, false>(run, unpack<DT>(raw), g);
         });
     }
-    Stats st = run.st;
+    Stats st = total(run);
     block_sums<TAIL>(st, li, lds, waves, wave, lane, g.c);
     if (g.parts > 1) {
         if (threadIdx.x == 0) a.part[row * g.parts + part] = make_float4(st.m, st.s, li.m, li.s);

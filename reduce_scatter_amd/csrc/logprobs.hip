@@ -218,14 +218,15 @@ __device__ __forceinline__ void gradient_vec(const VocabGeom<NR> &g, const RowGr
                                              const TileWalk &t, int e0, int held, u32x4 raw) {
     constexpr int K = Lanes<DT>::value;
     Pack<DT> x = unpack<DT>(raw);
-#pragma unroll
-    for (int i = 0; i < K; ++i) x.v[i] = rel(x.v[i], r.ref);
     if (r.a1 == 0.0f) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * r.a0;
+        for (int i = 0; i < K; ++i) x.v[i] = term<DT>(x.v[i], r.ref, g).e * r.a0;
     } else {
 #pragma unroll
-        for (int i = 0; i < K; ++i) x.v[i] = exp2_fast(x.v[i]) * __builtin_fmaf(hold_up(x.v[i]), r.a1, r.a0);
+        for (int i = 0; i < K; ++i) {
+            const Term y = term<DT>(x.v[i], r.ref, g);
+            x.v[i] = y.e * __builtin_fmaf(hold_up(y.t, kTLow), r.a1, r.a0);
+        }
     }
     if (t.at == r.p.t) {
         const int d = t.j * kTileElems<DT> + r.p.et - t.phase - held;
@@ -283,11 +284,12 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
                 best_col = t.col + max(e0, 0);
             }
         }
-        add_vec<DT, S1>(run, v, g.c);
+        if (u == 0) end_tile(run);
+        add_vec<DT, S1>(run, v, g);
     });
     float xt = 0.0f;
     if (wave == 0 && g.parts == 1 && target >= 0) xt = logit_at<DT>(g, row, target);
-    Stats st = run.st;
+    Stats st = total(run);
     block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
     const RowResult res = row_result(st);
     const long long slot = row * g.parts + part;

@@ -8,9 +8,8 @@
 // logit and 2^t one instruction; the rounding of y is the same for every
 // logit and cancels in every result, because results only use t and the sum
 // relative to the same y.  The reference need not be the maximum: a lane takes
-// its first vector's and keeps it while its sum stays below 2^16 (at most 2^14
-// terms of at most 1 if the reference is the maximum), so the stream takes no
-// maxima; a vector that carries the sum past that is added again after moving
+// its first vector's and keeps it while a tile's sum stays below 2^16, so the
+// stream takes no maxima; a vector that carries the sum past that is added again after moving
 // the reference.
 #pragma once
 
@@ -371,31 +370,77 @@ __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, long long row,
     return {s, e, t + at / kTileElems<DT>, at % kTileElems<DT>};
 }
 
-// A lane's running sums and reference.
+// t and 2^t of a logit.  In units of log2 a logit far below the reference
+// carries |t| 2^-24 of rounding into 2^t.  For 16-bit logits, whose gradients
+// are rounded to 2^-9 or 2^-12, that is nothing; for fp32 the product
+// (x - m) c is carried in two parts (c too), which leaves the rounding of
+// x - m itself.  Where x - m overflows the low part is no number and left out
+// (2^t is 0 or infinity then).
+struct Term {
+    float t, e;
+};
+__device__ __forceinline__ float hold_up(float t, float least) {
+    // one instruction: the builtin first quiets a signalling NaN, which no result of arithmetic is
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "s"(least), "v"(t));
+    return r;
+}
+template <int DT, int NR> __device__ __forceinline__ Term term(float x, const Ref &r, const VocabGeom<NR> &g) {
+    Term a;
+    if constexpr (DT == F32) {
+        const float d = x - (r.m == kNegInf ? 0.0f : r.m);
+        a.t = d * g.c;
+        const float lo = __builtin_fmaf(d, g.c_low, __builtin_fmaf(d, g.c, -a.t));
+        a.e = exp2_fast(a.t) * __builtin_fmaf(kLn2, __builtin_fabsf(lo) < 1.0f ? lo : 0.0f, 1.0f);
+    } else {
+        a.t = rel(x, r);
+        a.e = exp2_fast(a.t);
+    }
+    return a;
+}
+
+// A lane's running sums and reference: those of the tile at hand, and of the
+// tiles done, which are only added up tile by tile (a lane sees thousands of
+// terms, and each addition to the large sum would round it).
 struct Running {
     Stats st{kNegInf, 0.0f, 0.0f};
+    float done = 0.0f, done1 = 0.0f;
     Ref ref{kNegInf, 0.0f, 1.0f, false};
     int fresh = 1;                     // some lane has met no logit above -inf yet
 };
-// max(t, kTLow) as one instruction: the builtin first quiets a signalling
-// NaN, which no result of arithmetic is.
-__device__ __forceinline__ float hold_up(float t) {
-    float r;
-    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "s"(kTLow), "v"(t));
-    return r;
+__device__ __forceinline__ void end_tile(Running &a) {
+    a.done += a.st.s;
+    a.done1 += a.st.s1;
+    a.st.s = a.st.s1 = 0.0f;
 }
-// Add one vector's logits to a lane's sums.  2^t = 0 where t = -inf, but 0 * -inf is NaN: t is held above kTLow in the weighted
-// sum.
-template <int DT, bool S1> __device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v) {
+__device__ __forceinline__ Stats total(const Running &a) {
+    return Stats{a.st.m, a.done + a.st.s, a.done1 + a.st.s1};
+}
+// Add one vector's logits to a lane's sums.  2^t = 0 where t = -inf, but
+// 0 * -inf is NaN: t is held above kTLow in the weighted sum.
+template <int DT, bool S1, int NR>
+__device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v, const VocabGeom<NR> &g) {
+    constexpr int K = Lanes<DT>::value;
+    float e[K], s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < Lanes<DT>::value; ++i) {
-        const float t = rel(v.v[i], a.ref), e = exp2_fast(t);
-        a.st.s += e;
-        if constexpr (S1) a.st.s1 = __builtin_fmaf(e, hold_up(t), a.st.s1);
+    for (int i = 0; i < K; ++i) {
+        const Term x = term<DT>(v.v[i], a.ref, g);
+        e[i] = x.e;
+        if constexpr (S1) {
+            const float t = hold_up(x.t, kTLow);
+            s1 = i ? __builtin_fmaf(x.e, t, s1) : x.e * t;
+        }
     }
+#pragma unroll
+    for (int h = K / 2; h; h /= 2)
+#pragma unroll
+        for (int i = 0; i < h; ++i) e[i] += e[i + h];
+    a.st.s += e[0];
+    if constexpr (S1) a.st.s1 += s1;
 }
 // The same after moving the references of lanes whose vector has a larger maximum.
-template <int DT, bool S1> __device__ __forceinline__ void add_with_care(Running &a, Pack<DT> v, float c) {
+template <int DT, bool S1, int NR>
+__device__ __forceinline__ void add_with_care(Running &a, Pack<DT> v, const VocabGeom<NR> &g) {
     // other values to the compiler, which would otherwise take the first steps below for every vector
 #pragma unroll
     for (int i = 0; i < Lanes<DT>::value; ++i) asm volatile("" : "+v"(v.v[i]));
@@ -403,21 +448,26 @@ template <int DT, bool S1> __device__ __forceinline__ void add_with_care(Running
 #pragma unroll
     for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
     if (m > a.st.m) {
-        shift_stats(a.st, m, c);
-        a.ref = make_ref(m, c);
+        Stats done{a.st.m, a.done, a.done1};
+        shift_stats(a.st, m, g.c);
+        shift_stats(done, m, g.c);
+        a.done = done.s;
+        a.done1 = done.s1;
+        a.ref = make_ref(m, g.c);
     }
     a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
-    add_terms<DT, S1>(a, v);
+    add_terms<DT, S1>(a, v, g);
 }
 // Whether what has just been added has to be added again, with care: the
 // first vectors, and seldom later.
 __device__ __forceinline__ bool sums_off(const Running &a) { return (__ballot(a.st.s > 65536.0f) | (u64)a.fresh) != 0; }
-template <int DT, bool S1> __device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, float c) {
+template <int DT, bool S1, int NR>
+__device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, const VocabGeom<NR> &g) {
     const Stats before = a.st;
-    add_terms<DT, S1>(a, x);
+    add_terms<DT, S1>(a, x, g);
     if (sums_off(a)) {
         a.st = before;
-        add_with_care<DT, S1>(a, x, c);
+        add_with_care<DT, S1>(a, x, g);
     }
 }
 
@@ -474,24 +524,23 @@ template <int DT, int NR, int T> struct HeldTiles {
 template <int DT, bool S1, int NR, int T, typename F>
 __device__ __forceinline__ Stats held_sums(const VocabGeom<NR> &g, HeldTiles<DT, NR, T> &h, int lane, F prepare) {
     Running a;
-    Stats before = a.st;                                       // at the tile's start
     h.each(
         lane,
         [&](const TileWalk &t, int k, int u, int e0, int held, u32x4 &raw) {
             asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));         // after the vector before: few values live
             if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
             prepare(k, u, e0, held, raw);
-            add_terms<DT, S1>(a, unpack<DT>(raw));
+            add_terms<DT, S1>(a, unpack<DT>(raw), g);
         },
         [&](int k) {
             if (sums_off(a)) {
-                a.st = before;
+                a.st.s = a.st.s1 = 0.0f;                       // as at the tile's start
 #pragma unroll
-                for (int u = 0; u < kVocabU; ++u) add_with_care<DT, S1>(a, unpack<DT>(h.v[k * kVocabU + u]), g.c);
+                for (int u = 0; u < kVocabU; ++u) add_with_care<DT, S1>(a, unpack<DT>(h.v[k * kVocabU + u]), g);
             }
-            before = a.st;
+            end_tile(a);
         });
-    return a.st;
+    return total(a);
 }
 
 // ---- top-k ----------------------------------------------------------------

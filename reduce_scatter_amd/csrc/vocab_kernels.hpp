@@ -32,7 +32,7 @@ template <int NR> struct VocabGeom {
     int n, parts;
     int tiles;                         // of the row, over all ranks
     int skew;                          // 0, or where some row is off a 16-byte boundary a vector's elements less one
-    float c;                           // log2(e) / T
+    float c, c_low;                    // log2(e) / T, and what rounding it to c leaves
     float inv_t;                       // 1 / T
     long long row0;                    // first row of this launch
 };

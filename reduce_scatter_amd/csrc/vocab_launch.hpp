@@ -28,7 +28,9 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
     g.parts = c.parts;
     g.tiles = c.tiles;
     g.skew = c.skew;
-    g.c = (float)(1.4426950408889634 / (double)c.temperature);
+    const double scale = 1.4426950408889634 / (double)c.temperature;
+    g.c = (float)scale;
+    g.c_low = (float)(scale - (double)g.c);
     g.inv_t = (float)(1.0 / (double)c.temperature);
 }
 
