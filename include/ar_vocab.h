@@ -42,8 +42,7 @@
  * only has no distribution: ln p = -inf, entropy 0, distillation loss +inf,
  * gradients 0.  The lowest finite value is an ordinary number: a row of it is
  * uniform.  A NaN or +inf logit makes the row's results NaN.  A row whose
- * upstream gradients are all 0 gets a zero gradient without its logits being
- * read.
+ * upstream gradients are all 0 gets a zero gradient, whatever its logits.
  *
  * Arithmetic: fp32 throughout (maxima, sums, entropies, gradients); gradients
  * are rounded once, to nearest even, to the logits' type.  Sums are taken in

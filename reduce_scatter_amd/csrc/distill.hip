@@ -215,9 +215,9 @@ __device__ __forceinline__ void drop_listed(u32x4 &v, uint32_t bits, int u, int 
 // first form is stored everywhere; then, past a barrier, the workgroup stores
 // its listed columns once more, an entry to a thread.
 struct RowGradient {
-    Ref ref;
-    float gs, total, lse2, r2, cu;
-    bool zero, shifted;
+    Ref ref, all;                                  // of the unlisted terms, of the row's sum
+    float gs, total, lse2, cu;                     // cu includes 2^-r2
+    bool zero;
 };
 template <bool TAIL, int NR>
 __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, const DistillArgs &a, const Teacher &t,
@@ -225,31 +225,29 @@ __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, cons
     RowGradient d;
     d.gs = (a.grad_loss ? a.grad_loss[row] : 1.0f) * g.inv_t;
     d.zero = !t.live || d.gs == 0.0f || (r.m == kNegInf && r.s == 0.0f);
-    d.ref = make_ref(r.m, g.c);
+    d.ref = d.all = make_ref(r.m, g.c);
     d.total = t.total;
     d.lse2 = __builtin_log2f(r.s);
-    d.r2 = d.lse2;
+    float r2 = d.lse2;
     d.cu = t.total * d.gs;
     if constexpr (TAIL) {
         const bool none = r.tail2 == kNegInf;                  // no unlisted mass: nothing to scale
-        d.r2 = none ? 0.0f : r.tail2;
+        r2 = none ? 0.0f : r.tail2;
         d.cu = none ? 0.0f : (t.total * exp2_fast(r.tail2 - d.lse2) - t.qt) * d.gs;
+        if (r2 < -60.0f && !d.all.wide) {                      // far below the listed terms: from a reference down there
+            d.ref = make_ref(r.m + r2 / g.c, g.c);
+            r2 -= (d.ref.m - r.m) * g.c;
+        }
     }
-    d.shifted = d.r2 < -60.0f;                                 // 2^-r2 does not fit into the factor
-    if (!d.shifted) d.cu *= exp2_fast(-d.r2);
+    d.cu *= exp2_fast(-r2);
     return d;
 }
 template <int DT, int NR>
 __device__ __forceinline__ void gradient_vec(const VocabGeom<NR> &g, const RowGradient &d, long long row,
                                              const TileWalk &w, int e0, int held, u32x4 raw) {
     Pack<DT> v = unpack<DT>(raw);
-    if (d.shifted) {
 #pragma unroll
-        for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = exp2_fast(rel(v.v[i], d.ref) - d.r2) * d.cu;
-    } else {
-#pragma unroll
-        for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = term<DT>(v.v[i], d.ref, g).e * d.cu;
-    }
+    for (int i = 0; i < Lanes<DT>::value; ++i) v.v[i] = term<DT>(v.v[i], d.ref, g).e * d.cu;
     store_vec<DT>(grad_row_of<DT>(g, w.s, row), v, w, e0, held);
 }
 // The listed columns among the workgroup's tiles; an id's entries all store
@@ -267,7 +265,7 @@ __device__ __forceinline__ void store_listed(const VocabGeom<NR> &g, const Disti
             for (int i = 0; i < a.k; ++i)
                 if (l.place[i] == place) q += expf(ln_q(t, l.v[i]));
         }
-        const float p = d.total * exp2_fast(rel(l.z[k], d.ref) - d.lse2);
+        const float p = d.total * exp2_fast(rel(l.z[k], d.all) - d.lse2);
         store1<DT>(grad_row_of<DT>(g, l.s[k], row), l.e[k], round_to<DT>((p - q) * d.gs));
     });
 }
@@ -454,6 +452,7 @@ hipError_t run_distill(const VocabCall &c, const DistillArgs &a, VocabStage stag
         return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, false>, c.parts, c.waves, s);
     case kBoth:
         if (c.held == 1) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 1>, 1, c.waves, s);
+        if (c.held == 2) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 2>, 1, c.waves, s);
         if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s);
         return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true, true>, 1, c.waves, s);
     case kBackward: return launch_rows<NR>(c, a, distill_backward_kernel<DT, NR, TAIL>, c.parts, c.waves, s);

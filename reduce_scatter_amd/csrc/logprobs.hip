@@ -385,6 +385,9 @@ hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage st
     if (stage == kBoth && c.held == 1)
         return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, 1>, 1, c.waves, s)
                   : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, 1>, 1, c.waves, s);
+    if (stage == kBoth && c.held == 2)
+        return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, 2>, 1, c.waves, s)
+                  : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, 2>, 1, c.waves, s);
     if (stage == kBoth && c.held)
         return s1 ? launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, true, kHeldTiles>, 1, c.waves, s)
                   : launch_rows<NR>(c, a, logprobs_held_kernel<DT, NR, false, kHeldTiles>, 1, c.waves, s);

@@ -89,10 +89,21 @@ VocabCall short_rows(const Shape &s) {
 
 // Results and gradient in one launch: the row stays in registers where it
 // fits into 16 waves of four tiles (131072 columns of 16-bit logits, half that
-// in fp32) and those waves fill most of the 16 that a compute unit then holds.
+// in fp32): few rows take as few tiles a wave as they can, many rows four, if
+// `most` waves suffice and they fill most of the 16 that a compute unit then
+// holds.  Elsewhere the row is read twice.  Registers (reading twice), us:
+// cross-entropy 8192 x 32768 bf16 200 (233), 4096 x 131072 410 (473),
+// 8192 x 32768 fp32 388 (453); distillation with a tail 8192 x 32768 232 (274),
+// but 4096 x 131072, 16 waves of one row: 503 (475), and 8192 x 32768 fp32: 514
+// (471); cross-entropy 4096 x 100003, where 13 of the 16 waves are filled: 387 (379).
 VocabCall both_rows(const Shape &s, int most) {
     VocabCall c = s.c;
-    const int held = c.rows <= 256 && c.tiles <= kHeldWaves ? 1 : kHeldTiles, waves = (c.tiles + held - 1) / held;
+    int held = kHeldTiles;
+    if (c.rows <= 256) {
+        held = c.tiles <= kHeldWaves ? 1 : c.tiles <= 2 * kHeldWaves ? 2 : kHeldTiles;
+        most = kHeldWaves;
+    }
+    const int waves = (c.tiles + held - 1) / held;
     if (waves > most || (c.rows > 256 && kHeldWaves / waves * waves < 14)) return short_rows(s);
     c.held = held;
     c.waves = waves;
@@ -395,7 +406,8 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     a.saved = saved;
     a.grad_loss = grad_loss;
     const bool tail = mode == AR_TEACHER_TAIL;
-    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s, tail ? kHeldWaves / 2 : kHeldWaves), a, tail, kBoth, stream));
+    const int most = !tail ? kHeldWaves : s.c.dtype == AR_FLOAT32 ? 0 : kHeldWaves / 2;       // see both_rows
+    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s, most), a, tail, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     s.c.again = read_again(s, a.saved);

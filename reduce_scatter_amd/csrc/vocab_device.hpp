@@ -370,12 +370,12 @@ __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, long long row,
     return {s, e, t + at / kTileElems<DT>, at % kTileElems<DT>};
 }
 
-// t and 2^t of a logit.  In units of log2 a logit far below the reference
-// carries |t| 2^-24 of rounding into 2^t.  For 16-bit logits, whose gradients
-// are rounded to 2^-9 or 2^-12, that is nothing; for fp32 the product
-// (x - m) c is carried in two parts (c too), which leaves the rounding of
-// x - m itself.  Where x - m overflows the low part is no number and left out
-// (2^t is 0 or infinity then).
+// t and 2^t of a logit for its gradient.  In units of log2 a logit far below
+// the reference carries |t| 2^-24 of rounding into 2^t.  In the sums that
+// averages out, and gradients of 16-bit logits are rounded to 2^-9 or 2^-12;
+// for those of fp32 the product (x - m) c is carried in two parts (c too),
+// which leaves the rounding of x - m itself.  Where x - m overflows the low
+// part is no number and left out (2^t is 0 or infinity then).
 struct Term {
     float t, e;
 };
@@ -418,17 +418,16 @@ __device__ __forceinline__ Stats total(const Running &a) {
 }
 // Add one vector's logits to a lane's sums.  2^t = 0 where t = -inf, but
 // 0 * -inf is NaN: t is held above kTLow in the weighted sum.
-template <int DT, bool S1, int NR>
-__device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v, const VocabGeom<NR> &g) {
+template <int DT, bool S1> __device__ __forceinline__ void add_terms(Running &a, const Pack<DT> &v) {
     constexpr int K = Lanes<DT>::value;
     float e[K], s1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const Term x = term<DT>(v.v[i], a.ref, g);
-        e[i] = x.e;
+        const float t = rel(v.v[i], a.ref);
+        e[i] = exp2_fast(t);
         if constexpr (S1) {
-            const float t = hold_up(x.t, kTLow);
-            s1 = i ? __builtin_fmaf(x.e, t, s1) : x.e * t;
+            const float h = hold_up(t, kTLow);
+            s1 = i ? __builtin_fmaf(e[i], h, s1) : e[i] * h;
         }
     }
 #pragma unroll
@@ -456,7 +455,7 @@ __device__ __forceinline__ void add_with_care(Running &a, Pack<DT> v, const Voca
         a.ref = make_ref(m, g.c);
     }
     a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
-    add_terms<DT, S1>(a, v, g);
+    add_terms<DT, S1>(a, v);
 }
 // Whether what has just been added has to be added again, with care: the
 // first vectors, and seldom later.
@@ -464,7 +463,7 @@ __device__ __forceinline__ bool sums_off(const Running &a) { return (__ballot(a.
 template <int DT, bool S1, int NR>
 __device__ __forceinline__ void add_vec(Running &a, const Pack<DT> &x, const VocabGeom<NR> &g) {
     const Stats before = a.st;
-    add_terms<DT, S1>(a, x, g);
+    add_terms<DT, S1>(a, x);
     if (sums_off(a)) {
         a.st = before;
         add_with_care<DT, S1>(a, x, g);
@@ -530,7 +529,7 @@ __device__ __forceinline__ Stats held_sums(const VocabGeom<NR> &g, HeldTiles<DT,
             asm volatile("" : "+v"(raw), "+v"(a.st.s), "+v"(a.st.s1));         // after the vector before: few values live
             if (!t.template full<DT>()) mask_vec<DT>(raw, e0, held, t.w);
             prepare(k, u, e0, held, raw);
-            add_terms<DT, S1>(a, unpack<DT>(raw), g);
+            add_terms<DT, S1>(a, unpack<DT>(raw));
         },
         [&](int k) {
             if (sums_off(a)) {

@@ -62,7 +62,7 @@ struct VocabCall {
     int dtype;                         // ar::Dtype
     long long rows;
     int n, tiles, parts, waves;
-    int held;                          // kBoth: tiles per wave where a row fits in registers, 1 or kHeldTiles; 0: it does not
+    int held;                          // kBoth: tiles per wave where a row fits in registers, 1, 2 or kHeldTiles; 0: it does not
     int skew;                          // as VocabGeom's
     bool again;                        // kForward: a backward call on the same logits follows, and they fit the cache
     bool tiny;                         // a rank has columns, but not enough for one vector

@@ -231,6 +231,8 @@ SHAPES = [
     (3, [2049, 2047]), (2, [4101]), (300, [1000, 1001]), (260, [5000, 5003, 4999]), (1, [50021]),
     (2, [33000, 20, 0, 9001]), (3, [40000] * 5), (2, [37] * 17), (2, [3001] * 40 + [0] * 88), (1, [1]* 128),
     (7, [70001]),
+    # the largest vocabulary; a row in all of a workgroup's registers, with few rows and with many
+    (2, [1 << 20]), (20, [131072]), (257, [33000]),
 ]
 
 
