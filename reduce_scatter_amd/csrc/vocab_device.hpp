@@ -23,7 +23,6 @@ typedef unsigned long long u64;
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kTLow = -1e6f;         // stands for lower t (2^t = 0 far above it) where t multiplies 2^t: 0 * -inf is NaN
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
