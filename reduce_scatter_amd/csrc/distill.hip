@@ -107,16 +107,17 @@ struct RowSums {
     float m, s;                                    // reference, sum of 2^t
     float tail2;                                   // log2 of the unlisted part of the sum
 };
-// Unlisted and listed sums (each with its own reference) put together.
+// Unlisted and listed sums (each with its own reference) put together, relative to the larger one's logit.
 __device__ __forceinline__ RowSums join_sums(Stats tail, Stats listed, float c) {
     const float m = __builtin_fmaxf(tail.m, listed.m);
     const Ref to = make_ref(m, c);
+    const float d = residue(to), f = exp2_fast(-d);
     RowSums r;
     r.m = m;
-    r.tail2 = ref_shift(make_ref(tail.m, c), to, c) + __builtin_log2f(tail.s);
+    r.tail2 = ref_shift(make_ref(tail.m, c), to, c) - d + __builtin_log2f(tail.s);
     shift_stats(tail, m, c);
     shift_stats(listed, m, c);
-    r.s = tail.s + listed.s;
+    r.s = (tail.s + listed.s) * f;
     return r;
 }
 
@@ -219,7 +220,7 @@ struct RowGradient {
     float gs, total, lse2, cu;                     // cu includes 2^-r2
     bool zero;
 };
-template <bool TAIL, int NR>
+template <int DT, bool TAIL, int NR>
 __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, const DistillArgs &a, const Teacher &t,
                                                     const RowSums &r, long long row) {
     RowGradient d;
@@ -236,10 +237,10 @@ __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, cons
         d.cu = none ? 0.0f : (t.total * exp2_fast(r.tail2 - d.lse2) - t.qt) * d.gs;
         if (r2 < -60.0f && !d.all.wide) {                      // far below the listed terms: from a reference down there
             d.ref = make_ref(r.m + r2 / g.c, g.c);
-            r2 -= (d.ref.m - r.m) * g.c;
+            r2 -= rel_log2(d.ref.m, d.all, g.c);
         }
     }
-    d.cu *= exp2_fast(-r2);
+    d.cu *= exp2_fast(-r2 - term_shift<DT>(d.ref));
     return d;
 }
 template <int DT, int NR>
@@ -265,7 +266,7 @@ __device__ __forceinline__ void store_listed(const VocabGeom<NR> &g, const Disti
             for (int i = 0; i < a.k; ++i)
                 if (l.place[i] == place) q += expf(ln_q(t, l.v[i]));
         }
-        const float p = d.total * exp2_fast(rel(l.z[k], d.all) - d.lse2);
+        const float p = d.total * exp2_fast(rel_log2(l.z[k], d.all, g.c) - d.lse2);
         store1<DT>(grad_row_of<DT>(g, l.s[k], row), l.e[k], round_to<DT>((p - q) * d.gs));
     });
 }
@@ -372,7 +373,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
         if (lane == 0) write_row(a, row, r, loss);
     }
     if constexpr (BOTH)
-        gradient_tiles<DT>(g, a, row_gradient<TAIL>(g, a, t, r, row), t, list, row, part, first, step, lane);
+        gradient_tiles<DT>(g, a, row_gradient<DT, TAIL>(g, a, t, r, row), t, list, row, part, first, step, lane);
 }
 
 // Loss and gradient of a row held in the workgroup's registers: 8192 x 32768
@@ -406,7 +407,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void distill_held_kernel(const Voc
         const float loss = row_loss<TAIL>(g, a, t, list, r, lane);
         if (lane == 0) write_row(a, row, r, loss);
     }
-    const RowGradient d = row_gradient<TAIL>(g, a, t, r, row);
+    const RowGradient d = row_gradient<DT, TAIL>(g, a, t, r, row);
     if (d.zero) {
         zero_tiles<DT>(g, row, wave, waves, lane);
         return;
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_backward_kernel(cons
     const long long row = g.row0 + local;
     const Teacher t = load_teacher<DT, TAIL>(g, a, list, row, lane);
     const float *o = a.saved + row * 4;
-    const RowGradient d = row_gradient<TAIL>(g, a, t, RowSums{o[0], o[1], o[2]}, row);
+    const RowGradient d = row_gradient<DT, TAIL>(g, a, t, RowSums{o[0], o[1], o[2]}, row);
     gradient_tiles<DT>(g, a, d, t, list, row, part, part * waves + wave, step, lane);
 }
 

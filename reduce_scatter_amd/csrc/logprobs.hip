@@ -190,9 +190,10 @@ __device__ __forceinline__ void select_top(const VocabGeom<NR> &g, long long row
     if (thread < k) emit(thread, v);
 }
 
-// Gradient of a row: with e = 2^t and p = e / S,
+// Gradient of a row: with e = 2^t and p = e / S, t relative to m,
 //   dx = [v = target] gl/T + e * (a0 + a1 t),
-//   a0 = -(gl + gh (H - ln S)) / (T S),  a1 = -gh ln2 / (T S).
+//   a0 = -(gl + gh (H - ln S)) / (T S),  a1 = -gh ln2 / (T S),
+// and where term() gives t + d instead: a0 - d a1 for a0, both times 2^-d.
 struct RowGradient {
     Ref ref;
     float a0, a1, at_target;
@@ -208,6 +209,11 @@ __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, cons
     r.ref = make_ref(st.m, g.c);
     r.a0 = -(gl + gh * (res.entropy - res.lse)) * g.inv_t / st.s;
     r.a1 = -gh * kLn2 * g.inv_t / st.s;
+    if constexpr (DT != F32) {
+        const float d = term_shift<DT>(r.ref), f = exp2_fast(-d);
+        r.a0 = __builtin_fmaf(-d, r.a1, r.a0) * f;
+        r.a1 *= f;
+    }
     r.at_target = gl * g.inv_t;
     r.p = target >= 0 ? place_of<DT>(g, row, target) : Place{0, 0, -1, 0};
     r.zero = res.empty || (gl == 0.0f && gh == 0.0f);
@@ -293,12 +299,13 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_kernel(const VocabG
     });
     float xt = 0.0f;
     if (wave == 0 && g.parts == 1 && target >= 0) xt = logit_at<DT>(g, row, target);
-    Stats st = total(run);
-    block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
+    Stats sum = total(run);
+    block_stats<S1>(sum, lds_stats, waves, wave, lane, g.c);
+    const Stats st = settled(sum, g.c);
     const RowResult res = row_result(st);
     const long long slot = row * g.parts + part;
     if (threadIdx.x == 0) {
-        if (g.parts > 1) a.part[slot] = make_float4(st.m, st.s, st.s1, 0.0f);
+        if (g.parts > 1) a.part[slot] = make_float4(sum.m, sum.s, sum.s1, 0.0f);
         else write_row(g, a, row, st, res, xt, target >= 0);
     }
     if constexpr (TOP) {
@@ -327,6 +334,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void logprobs_join_kernel(const V
         st = Stats{p.x, p.y, p.z};
     }
     wave_stats<S1>(st, lane, g.c);
+    st = settled(st, g.c);
     const RowResult res = row_result(st);
     if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
     if constexpr (TOP) {
@@ -374,6 +382,7 @@ __global__ __launch_bounds__(64 * kHeldWaves) void logprobs_held_kernel(const Vo
     const float xt = wave == 0 && target >= 0 ? logit_at<DT>(g, row, target) : 0.0f;
     Stats st = held_sums<DT, S1>(g, tiles, lane, [](int, int, int, int, u32x4 &) {});
     block_stats<S1>(st, lds_stats, waves, wave, lane, g.c);
+    st = settled(st, g.c);
     const RowResult res = row_result(st);
     if (threadIdx.x == 0) write_row(g, a, row, st, res, xt, target >= 0);
     const RowGradient r = row_gradient<DT>(g, a, row, st, res, target);

@@ -6,8 +6,9 @@
 // Statistics are kept in units of log2: with c = log2(e) / T and a reference
 // logit m, t = x*c - y, y = m*c rounded once, is one fused multiply-add per
 // logit and 2^t one instruction; the rounding of y is the same for every
-// logit and cancels in every result, because results only use t and the sum
-// relative to the same y.  The reference need not be the maximum: a lane takes
+// logit, so sums stand against y as they are joined, and a row's whole sums are
+// taken to m itself (settled) before any result or gradient uses them.  The
+// reference need not be the maximum: a lane takes
 // its first vector's and keeps it while a tile's sum stays below 2^16, so the
 // stream takes no maxima; a vector that carries the sum past that is added again after moving
 // the reference.
@@ -46,10 +47,18 @@ __device__ __forceinline__ Ref make_ref(float m, float c) {
     return r;
 }
 __device__ __forceinline__ float rel(float x, const Ref &r) { return __builtin_fmaf(x, r.c, -r.y); }
-// (x - m) / T in natural units, also where t overflows or has the other scale.
+// t at x = m: what rounding y took away, exactly.
+__device__ __forceinline__ float residue(const Ref &r) {
+    return r.wide || r.m == kNegInf ? 0.0f : __builtin_fmaf(r.m, r.c, -r.y);
+}
+// (x - m) / T in natural units and in units of log2, also where t overflows or has the other scale.
 __device__ __forceinline__ float rel_ln(float x, const Ref &r, float inv_t) {
     const float t = rel(x, r);
-    return finite(t) && !r.wide ? kLn2 * t : (x - r.m) * inv_t;
+    return finite(t) && !r.wide ? kLn2 * (t - residue(r)) : (x - r.m) * inv_t;
+}
+__device__ __forceinline__ float rel_log2(float x, const Ref &r, float c) {
+    const float t = rel(x, r);
+    return finite(t) && !r.wide ? t - residue(r) : (x - r.m) * c;
 }
 // log2 of the factor that takes sums relative to `from` to reference `to` (to.m >= from.m).
 __device__ __forceinline__ float ref_shift(const Ref &from, const Ref &to, float c) {
@@ -68,6 +77,13 @@ __device__ __forceinline__ void shift_stats(Stats &a, float to, float c) {
     a.s1 = f == 0.0f ? 0.0f : f * __builtin_fmaf(a.s, d, a.s1);
     a.s *= f;
     a.m = to;
+}
+
+// A row's whole sums relative to its reference logit m instead of y: what rel_ln
+// and the fp32 terms (term) count from, and what a caller is given.
+__device__ __forceinline__ Stats settled(const Stats &a, float c) {
+    const float r = residue(make_ref(a.m, c)), f = exp2_fast(-r);
+    return Stats{a.m, a.s * f, __builtin_fmaf(a.s, -r, a.s1) * f};
 }
 
 // The value of lane (lane ^ M): data-parallel moves within rows of 16 lanes,
@@ -371,9 +387,10 @@ __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, long long row,
 
 // t and 2^t of a logit for its gradient.  In units of log2 a logit far below
 // the reference carries |t| 2^-24 of rounding into 2^t.  In the sums that
-// averages out, and gradients of 16-bit logits are rounded to 2^-9 or 2^-12;
-// for those of fp32 the product (x - m) c is carried in two parts (c too),
-// which leaves the rounding of x - m itself.  Where x - m overflows the low
+// averages out, and gradients of 16-bit logits are rounded to 2^-9 or 2^-12,
+// so these take t relative to y (term_shift() of the reference off); for
+// those of fp32 the product (x - m) c is carried in two parts (c too), which
+// leaves the rounding of x - m itself.  Where x - m overflows the low
 // part is no number and left out (2^t is 0 or infinity then).
 struct Term {
     float t, e;
@@ -397,6 +414,9 @@ template <int DT, int NR> __device__ __forceinline__ Term term(float x, const Re
     }
     return a;
 }
+
+// What t in term() is too large by: a row's factors take it away, not each logit.
+template <int DT> __device__ __forceinline__ float term_shift(const Ref &r) { return DT == F32 ? 0.0f : residue(r); }
 
 // A lane's running sums and reference: those of the tile at hand, and of the
 // tiles done, which are only added up tile by tile (a lane sees thousands of
