@@ -102,23 +102,21 @@ __device__ __forceinline__ Teacher load_teacher(const VocabGeom<NR> &g, const Di
     return t;
 }
 
-// Sums of a row: every entry's, and the unlisted entries' as a logarithm.
+// Sums of a row, each relative to its own reference logit: every entry's and
+// the unlisted entries'.  The unlisted ones keep theirs, because they may lie
+// any distance below the row's: one number for both would lose their count.
 struct RowSums {
-    float m, s;                                    // reference, sum of 2^t
-    float tail2;                                   // log2 of the unlisted part of the sum
+    float m, s;
+    float tm, ts;
 };
-// Unlisted and listed sums (each with its own reference) put together, relative to the larger one's logit.
+// Unlisted and listed sums (each with its own reference) put together.
 __device__ __forceinline__ RowSums join_sums(Stats tail, Stats listed, float c) {
+    const Stats rest = settled(tail, c);
     const float m = __builtin_fmaxf(tail.m, listed.m);
-    const Ref to = make_ref(m, c);
-    const float d = residue(to), f = exp2_fast(-d);
-    RowSums r;
-    r.m = m;
-    r.tail2 = ref_shift(make_ref(tail.m, c), to, c) - d + __builtin_log2f(tail.s);
     shift_stats(tail, m, c);
     shift_stats(listed, m, c);
-    r.s = (tail.s + listed.s) * f;
-    return r;
+    const Stats all = settled(Stats{m, tail.s + listed.s, 0.0f}, c);
+    return {all.m, all.s, rest.m, rest.s};
 }
 
 // How many of the first n entries stand at `place`, eight reads at a time (each waits for LDS).
@@ -146,7 +144,8 @@ __device__ __forceinline__ float row_loss(const VocabGeom<NR> &g, const DistillA
     }
     sum = wave_sum(sum, lane);
     if constexpr (TAIL) {
-        if (t.qt != 0.0f) sum += t.qt * (logf(t.qt) - (empty ? kNegInf : kLn2 * r.tail2 - lse));
+        const float lt = empty ? kNegInf : rel_ln(r.tm, ref, g.inv_t) + (logf(r.ts) - lse);
+        if (t.qt != 0.0f) sum += t.qt * (logf(t.qt) - lt);
     }
     return t.live ? sum : 0.0f;
 }
@@ -157,8 +156,8 @@ __device__ __forceinline__ void write_row(const DistillArgs &a, long long row, c
         float *o = a.saved + row * 4;
         o[0] = r.m;
         o[1] = r.s;
-        o[2] = r.tail2;
-        o[3] = 0.0f;
+        o[2] = r.tm;
+        o[3] = r.ts;
     }
 }
 
@@ -208,16 +207,16 @@ __device__ __forceinline__ void drop_listed(u32x4 &v, uint32_t bits, int u, int 
     }
 }
 
-// Gradient of a row:
-//   unlisted  2^(t - r2) * cu,  listed  (Q 2^(t - lse2) - q_v) * g / T,
-// where r2 is the log2 of the unlisted sum and cu = (Q tail / S - q_t) g / T
-// (TAIL), or of the whole sum and cu = Q g / T.  Referred to their own sum,
-// the unlisted terms keep their precision however small their share is.  The
+// Gradient of a row, t relative to m (listed) or to the unlisted entries' m_t:
+//   unlisted  2^t * cu,  listed  (Q 2^t / S - q_v) * g / T,
+// with cu = (Q p_t - q_t) g / (T S_t), p_t = 2^((m_t - m) c) S_t / S (TAIL), or,
+// both against the whole row, cu = Q g / (T S).  Referred to their own sum, the
+// unlisted terms keep their precision however small their share is.  The
 // first form is stored everywhere; then, past a barrier, the workgroup stores
 // its listed columns once more, an entry to a thread.
 struct RowGradient {
     Ref ref, all;                                  // of the unlisted terms, of the row's sum
-    float gs, total, lse2, cu;                     // cu includes 2^-r2
+    float gs, total, lse2, cu;
     bool zero;
 };
 template <int DT, bool TAIL, int NR>
@@ -229,18 +228,14 @@ __device__ __forceinline__ RowGradient row_gradient(const VocabGeom<NR> &g, cons
     d.ref = d.all = make_ref(r.m, g.c);
     d.total = t.total;
     d.lse2 = __builtin_log2f(r.s);
-    float r2 = d.lse2;
-    d.cu = t.total * d.gs;
     if constexpr (TAIL) {
-        const bool none = r.tail2 == kNegInf;                  // no unlisted mass: nothing to scale
-        r2 = none ? 0.0f : r.tail2;
-        d.cu = none ? 0.0f : (t.total * exp2_fast(r.tail2 - d.lse2) - t.qt) * d.gs;
-        if (r2 < -60.0f && !d.all.wide) {                      // far below the listed terms: from a reference down there
-            d.ref = make_ref(r.m + r2 / g.c, g.c);
-            r2 -= rel_log2(d.ref.m, d.all, g.c);
-        }
+        const float pt = exp2_fast(rel_log2(r.tm, d.all, g.c)) * (r.ts / r.s);
+        d.ref = make_ref(r.tm, g.c);
+        d.cu = r.ts == 0.0f ? 0.0f : (t.total * pt - t.qt) * d.gs / r.ts;          // no unlisted mass: nothing to scale
+    } else {
+        d.cu = t.total * d.gs / r.s;
     }
-    d.cu *= exp2_fast(-r2 - term_shift<DT>(d.ref));
+    d.cu *= exp2_fast(-term_shift<DT>(d.ref));
     return d;
 }
 template <int DT, int NR>
@@ -446,7 +441,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_backward_kernel(cons
     const long long row = g.row0 + local;
     const Teacher t = load_teacher<DT, TAIL>(g, a, list, row, lane);
     const float *o = a.saved + row * 4;
-    const RowGradient d = row_gradient<DT, TAIL>(g, a, t, RowSums{o[0], o[1], o[2]}, row);
+    const RowGradient d = row_gradient<DT, TAIL>(g, a, t, RowSums{o[0], o[1], o[2], o[3]}, row);
     gradient_tiles<DT>(g, a, d, t, list, row, part, part * waves + wave, step, lane);
 }
 
