@@ -106,14 +106,16 @@ def distill_grad(x, temperature, ids, values, tail, g):
     logp, empty = log_softmax(x, temperature)
     rows, vocab = logp.shape
     q, _, valid, qt, live = teacher(ids, values, vocab, tail, temperature)
-    _, _, lt = distill(x, temperature, ids, values, tail)
     dense = np.zeros((rows, vocab))
     r, k = np.nonzero(valid)
     np.add.at(dense, (r, ids[r, k]), q[r, k])
     with np.errstate(all="ignore"):
         out = (q.sum(1) + qt)[:, None] * np.exp(logp) - dense
-        rest = np.where(_unlisted(ids, valid, vocab), logp, -np.inf)
-        cond = np.where(rest == -np.inf, 0.0, np.exp(rest - np.where(lt == -np.inf, 0.0, lt)[:, None]))
+        # shares of the unlisted mass against its own largest entry: at -1e38 a logarithm has lost their number
+        rest = np.where(_unlisted(ids, valid, vocab), np.asarray(x, dtype=np.float64), -np.inf)
+        most = rest.max(1, keepdims=True)
+        share = np.exp((rest - np.where(most == -np.inf, 0.0, most)) / temperature)
+        cond = np.where(rest == -np.inf, 0.0, share / share.sum(1, keepdims=True))
         out = (out - qt[:, None] * cond) * (np.asarray(g, dtype=np.float64) / temperature)[:, None]
     out[empty | ~live | (np.asarray(g) == 0)] = 0.0
     return out
