@@ -30,20 +30,28 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_huge_valf(); }
 
 // The reference of a set of logits: t = x*c - y.  m = -inf (nothing but masked
-// logits) counts from 0.  Where m is so large that m*c overflows (a row of the
-// lowest value, say), c is 1 and t = x - m: any other number is then at least
-// 2^104 away, so 2^t is 1 or 0 under either scale.
+// logits) counts from 0.  For x = m that leaves t = residue(), what rounding y
+// took away: up to half a unit in the last place of m*c.  That is no more than 32 while
+// |m*c| is below 2^30, but hundreds and more beyond (masks of -1e10, or any
+// logit at a temperature near 0), infinity or zero to 2^t.  From 2^30 on c
+// therefore is the power of two that puts |m| c into [2^30, 2^31): the product is
+// exact, t = 0 at x = m, and any other number is a unit in m's last place
+// away, 2^6 at least in t under either scale, where 2^t counts for nothing
+// beside 1 (2^20 columns of it are 2^-44).
 struct Ref {
     float m, y, c;
-    bool wide;                         // c is 1 instead of log2(e) / T
+    bool wide;                         // c is that power of two instead of log2(e) / T
 };
 __device__ __forceinline__ Ref make_ref(float m, float c) {
     Ref r;
     r.m = m;
+    r.c = c;
     r.y = m == kNegInf ? 0.0f : m * c;
-    r.wide = finite(m) && !finite(r.y);
-    r.y = r.wide ? m : r.y;
-    r.c = r.wide ? 1.0f : c;
+    r.wide = finite(m) && __builtin_fabsf(r.y) >= 0x1p30f;
+    if (r.wide) {
+        r.c = __builtin_amdgcn_ldexpf(1.0f, 31 - __builtin_amdgcn_frexp_expf(m));
+        r.y = m * r.c;
+    }
     return r;
 }
 __device__ __forceinline__ float rel(float x, const Ref &r) { return __builtin_fmaf(x, r.c, -r.y); }
@@ -64,7 +72,7 @@ __device__ __forceinline__ float rel_log2(float x, const Ref &r, float c) {
 __device__ __forceinline__ float ref_shift(const Ref &from, const Ref &to, float c) {
     if (from.m == to.m) return 0.0f;
     if (from.m == kNegInf) return kNegInf;
-    return (from.wide || to.wide) ? (from.m - to.m) * c : from.y - to.y;
+    return from.wide || to.wide ? (from.m - to.m) * c + (residue(to) - residue(from)) : from.y - to.y;
 }
 
 // Sums of 2^t and t*2^t, and where the sums stand.

@@ -46,7 +46,7 @@ def check_all_calls(d, targets, k, gl, gh, ids, vals, keep=None):
 @pytest.mark.parametrize("rows, widths", [(5, [3000, 1001]), (5, [60000]), (258, [1100, 1101])])
 @pytest.mark.parametrize("offset, temperature", [
     (0.0, 1.0), (0.0, 0.01), (10.0, 1.0), (10.0, 0.01), (100.0, 1.0), (100.0, 0.01), (1000.0, 1.0), (-1000.0, 0.01),
-    (1e6, 1.0), (1e6, 0.01), (-1e8, 1.0), (7e8, 1.0),
+    (1e6, 1.0), (1e6, 0.01), (-1e8, 1.0), (-1e8, 0.01), (7e8, 1.0), (7e8, 0.01),
 ])
 def test_gradients(offset, temperature, rows, widths):
     rng = np.random.default_rng(33)
@@ -66,7 +66,7 @@ def test_gradients(offset, temperature, rows, widths):
 
 @pytest.mark.parametrize("dtype, rows, widths, offset", [
     ("f32", 3, [3000, 1001], 0.0), ("f32", 3, [3000, 1001], 1000.0), ("f32", 3, [60000], -1e6),
-    ("f32", 258, [2100], 5e8), ("bf16", 3, [3000, 1001], 30.0), ("f16", 3, [60000], -900.0),
+    ("f32", 258, [2100], 5e8), ("f32", 3, [2048], -1e9), ("bf16", 3, [3000, 1001], 30.0), ("f16", 3, [60000], -900.0),
 ])
 def test_saved_is_a_logit_and_its_sum(dtype, rows, widths, offset):
     """saved[:, 0] and saved[:, 1] as the header states them: m and sum_v exp((x_v - m) / T)."""

@@ -44,7 +44,7 @@ def distill(d, ids, vals, g, fused):
 
 @pytest.mark.parametrize("rows, widths", [(4, [700, 701]), (4, [60000]), (258, [1100, 1101])])
 @pytest.mark.parametrize("temperature", [1.0, 2.0])
-@pytest.mark.parametrize("fill", [-6e4, -1e4, -1e3])
+@pytest.mark.parametrize("fill", ["lowest", -6e4, -1e4, -1e3])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_every_unlisted_entry_masked(dtype, fill, temperature, rows, widths):
     rng = np.random.default_rng(41)
