@@ -25,6 +25,7 @@ typedef unsigned long long u64;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kTLow = -1e6f;         // stands for lower t (2^t = 0 far above it) where t multiplies 2^t: 0 * -inf is NaN
+constexpr float kWide = 0x1p30f;       // see make_ref
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_huge_valf(); }
@@ -47,7 +48,7 @@ __device__ __forceinline__ Ref make_ref(float m, float c) {
     r.m = m;
     r.c = c;
     r.y = m == kNegInf ? 0.0f : m * c;
-    r.wide = finite(m) && __builtin_fabsf(r.y) >= 0x1p30f;
+    r.wide = finite(m) && __builtin_fabsf(r.y) >= kWide;
     if (r.wide) {
         r.c = __builtin_amdgcn_ldexpf(1.0f, 31 - __builtin_amdgcn_frexp_expf(m));
         r.y = m * r.c;
@@ -79,12 +80,19 @@ __device__ __forceinline__ float ref_shift(const Ref &from, const Ref &to, float
 struct Stats {
     float m, s, s1;
 };
-__device__ __forceinline__ void shift_stats(Stats &a, float to, float c) {
-    const float d = ref_shift(make_ref(a.m, c), make_ref(to, c), c);
-    const float f = exp2_fast(d);
+// To the reference logit `to`, d = log2 of the factor f.
+__device__ __forceinline__ void shift_by(Stats &a, float to, float d, float f) {
     a.s1 = f == 0.0f ? 0.0f : f * __builtin_fmaf(a.s, d, a.s1);
     a.s *= f;
     a.m = to;
+}
+// ref_shift without making the references, unless some lane's is wide.
+__device__ __forceinline__ void shift_stats(Stats &a, float to, float c) {
+    const float from_y = a.m * c, to_y = to * c;
+    const bool wide = (finite(a.m) && __builtin_fabsf(from_y) >= kWide) || (finite(to) && __builtin_fabsf(to_y) >= kWide);
+    float d = a.m == to ? 0.0f : from_y - to_y;
+    if (__builtin_expect(__any(wide), 0)) d = ref_shift(make_ref(a.m, c), make_ref(to, c), c);
+    shift_by(a, to, d, exp2_fast(d));
 }
 
 // A row's whole sums relative to its reference logit m instead of y: what rel_ln
@@ -474,12 +482,14 @@ __device__ __forceinline__ void add_with_care(Running &a, Pack<DT> v, const Voca
 #pragma unroll
     for (int i = 1; i < Lanes<DT>::value; ++i) m = __builtin_fmaxf(m, v.v[i]);
     if (m > a.st.m) {
+        const Ref to = make_ref(m, g.c);
+        const float d = ref_shift(a.ref, to, g.c), f = exp2_fast(d);
         Stats done{a.st.m, a.done, a.done1};
-        shift_stats(a.st, m, g.c);
-        shift_stats(done, m, g.c);
+        shift_by(a.st, m, d, f);
+        shift_by(done, m, d, f);
         a.done = done.s;
         a.done1 = done.s1;
-        a.ref = make_ref(m, g.c);
+        a.ref = to;
     }
     a.fresh = __builtin_amdgcn_readfirstlane(__any(a.st.m == kNegInf));
     add_terms<DT, S1>(a, v);
