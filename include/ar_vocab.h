@@ -23,17 +23,17 @@
  * (gl counts as 0 in a row without a token).
  *
  * Distillation (ar_distill), per row, from K teacher entries (id i_k, value
- * t_k); entries whose id is outside [0, V) are padding, a repeated id adds its
- * entries' probabilities:
+ * t_k); entries whose id is outside [0, V) are padding:
  *   AR_TEACHER_RENORM  q = softmax(t / T) over the entries, q_t = 0;
  *   AR_TEACHER_TAIL    the values are log probabilities (at temperature T) out
  *                 of the whole vocabulary: q_k = exp(t_k), and the remaining
  *                 mass q_t = 1 - sum q (0 when below 2^-20, where it is only
  *                 the rounding of the values) is compared with the student's
  *                 mass p_t on all entries that are not listed.
- *   loss  sum_k q_k (ln q_k - ln p[i_k]) + q_t (ln q_t - ln p_t)
- *                 (the Kullback-Leibler divergence; terms with q = 0 are 0)
- *   dx_v  g/T * (Q p_v - sum_{k: i_k = v} q_k - [v not listed] q_t p_v / p_t),
+ *   A repeated id adds its entries' probabilities: Q_v = sum of q_k over i_k = v.
+ *   loss  sum_v Q_v (ln Q_v - ln p_v) + q_t (ln q_t - ln p_t) over the listed v
+ *                 (the Kullback-Leibler divergence; terms with Q_v = 0 are 0)
+ *   dx_v  g/T * (Q p_v - Q_v - [v not listed] q_t p_v / p_t),
  *                 Q = sum q + q_t, g the upstream gradient of the row's loss
  *   A row with no entry in [0, V) (renormalised: none above -inf) has loss 0
  *   and gradient 0.

@@ -87,14 +87,26 @@ def _unlisted(ids, valid, vocab):
     return out
 
 
+def _by_id(ids, valid, q, vocab):
+    """[rows, V] probabilities of the teacher: a repeated id adds its entries'."""
+    dense = np.zeros((len(ids), vocab))
+    r, k = np.nonzero(valid)
+    np.add.at(dense, (r, ids[r, k]), q[r, k])
+    return dense
+
+
 def distill(x, temperature, ids, values, tail):
     """(loss, ln p at the listed ids, ln of the unlisted mass)."""
     logp, _ = log_softmax(x, temperature)
     vocab = logp.shape[1]
     q, lq, valid, qt, live = teacher(ids, values, vocab, tail, temperature)
-    lpk = np.take_along_axis(logp, np.where(valid, ids, 0), 1)
+    at = np.where(valid, ids, 0)
+    lpk = np.take_along_axis(logp, at, 1)
     with np.errstate(all="ignore"):
-        loss = np.where(q == 0, 0.0, q * (lq - lpk)).sum(1)
+        # an id that stands once keeps the logarithm it was given
+        dense = _by_id(ids, valid, q, vocab)
+        total = np.take_along_axis(dense, at, 1)
+        loss = np.where(q == 0, 0.0, q * (np.where(total == q, lq, np.log(total)) - lpk)).sum(1)
         rest = np.where(_unlisted(ids, valid, vocab), logp, -np.inf)
         m = rest.max(1)
         lt = np.where(m == -np.inf, -np.inf, m + np.log(np.exp(rest - np.where(m == -np.inf, 0, m)[:, None]).sum(1)))
@@ -106,9 +118,7 @@ def distill_grad(x, temperature, ids, values, tail, g):
     logp, empty = log_softmax(x, temperature)
     rows, vocab = logp.shape
     q, _, valid, qt, live = teacher(ids, values, vocab, tail, temperature)
-    dense = np.zeros((rows, vocab))
-    r, k = np.nonzero(valid)
-    np.add.at(dense, (r, ids[r, k]), q[r, k])
+    dense = _by_id(ids, valid, q, vocab)
     with np.errstate(all="ignore"):
         out = (q.sum(1) + qt)[:, None] * np.exp(logp) - dense
         # shares of the unlisted mass against its own largest entry: at -1e38 a logarithm has lost their number

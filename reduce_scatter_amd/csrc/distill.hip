@@ -19,11 +19,25 @@ constexpr int kPer = kTeacherMax / 64;             // entries per lane, where a 
 
 // A row's list in LDS.
 struct ListScratch {
-    int place[kTeacherMax];                        // tile * kTileElems + element there (-1: padding)
+    alignas(16) int place[kTeacherMax];            // tile * kTileElems + element there (-1: padding, also to a multiple of 4)
     int s[kTeacherMax], e[kTeacherMax];            // rank and element there
     float v[kTeacherMax];                          // the teacher's value
     float z[kTeacherMax];                          // the student's logit, read before any gradient is stored
+    int repeats;                                   // some id stands more than once
 };
+// Places by hash, to find out whether any repeats: slots for k entries, a power
+// of two, four times as many (looks are then short) but no more than twice the
+// longest list.  The launch asks for this LDS, because the longest list's
+// would keep workgroups of one wave from filling a compute unit.
+__host__ __device__ inline int slot_bits(int k) {
+    static_assert(kTeacherMax == 256, "9 bits");
+    const int bits = 32 - __builtin_clz(4 * k - 1);
+    return bits < 6 ? 6 : bits > 9 ? 9 : bits;
+}
+__device__ __forceinline__ int *place_table() {
+    extern __shared__ int table[];
+    return table;
+}
 
 // The teacher's distribution (uniform over the workgroup): ln q = (v - m) * scale - ls.
 struct Teacher {
@@ -55,6 +69,9 @@ __device__ __forceinline__ Teacher load_teacher(const VocabGeom<NR> &g, const Di
         l.v[k] = in ? v : kNegInf;
         l.z[k] = in ? load1<DT>(row_of<DT>(g, p.s, row), p.e) : kNegInf;
     });
+    if (threadIdx.x < (unsigned)(-a.k & 3)) l.place[a.k + threadIdx.x] = -1;
+    for (int i = threadIdx.x; i < 1 << slot_bits(a.k); i += blockDim.x) place_table()[i] = -1;
+    if (threadIdx.x == 0) l.repeats = 0;
     __syncthreads();
     Teacher t;
     float sum = 0.0f, m = kNegInf;
@@ -119,17 +136,45 @@ __device__ __forceinline__ RowSums join_sums(Stats tail, Stats listed, float c) 
     return {all.m, all.s, rest.m, rest.s};
 }
 
-// How many of the first n entries stand at `place`, eight reads at a time (each waits for LDS).
-__device__ __forceinline__ int count_entries(const ListScratch &l, int n, int place) {
-    int same = 0;
-    for (int i = 0; i < n; i += 8) {
-#pragma unroll
-        for (int b = 0; b < 8; ++b) same += (l.place[i + b] == place) & (i + b < n);   // the array's length is a multiple of 8
+// Whether any id repeats, in l.repeats past the next barrier (all threads,
+// after load_teacher): every entry looks for its place in the table, which
+// takes a look or two; comparing each with the whole list is left to those
+// rows where it says so.
+__device__ __forceinline__ void note_repeats(const DistillArgs &a, ListScratch &l) {
+    const int bits = slot_bits(a.k);
+    each_entry(a, [&](int k) {
+        const int place = l.place[k];
+        if (place < 0) return;
+        for (unsigned h = (unsigned)place * 2654435761u >> (32 - bits);; h = (h + 1) & ((1u << bits) - 1)) {
+            const int there = atomicCAS(&place_table()[h], -1, place);
+            if (there == place) l.repeats = 1;
+            if (there == place || there == -1) return;         // there are free slots always
+        }
+    });
+}
+// f(i) for every entry i of the list that stands at `place`, in order.
+template <typename F> __device__ __forceinline__ void each_at(const ListScratch &l, int n, int place, F f) {
+    for (int i = 0; i < n; i += 4) {
+        const int4 p = *(const int4 *)(l.place + i);
+        if (p.x == place) f(i);
+        if (p.y == place) f(i + 1);
+        if (p.z == place) f(i + 2);
+        if (p.w == place) f(i + 3);
     }
-    return same;
+}
+// ln q of entry k's id: a repeated one's entries are added up.
+__device__ __forceinline__ float ln_q_of_id(const DistillArgs &a, const Teacher &t, const ListScratch &l, int k) {
+    const int place = l.place[k];
+    const float lq = ln_q(t, l.v[k]);
+    if (!l.repeats || place < 0) return lq;
+    float q = 0.0f;
+    int same = 0;
+    each_at(l, a.k, place, [&](int i) { q += expf(ln_q(t, l.v[i])), ++same; });
+    return same > 1 ? logf(q) : lq;
 }
 
-// The row's loss, in all lanes of the wave.
+// The row's loss, in all lanes of the wave.  An entry counts its own q times
+// the logarithm of its id's.
 template <bool TAIL, int NR>
 __device__ __forceinline__ float row_loss(const VocabGeom<NR> &g, const DistillArgs &a, const Teacher &t,
                                           const ListScratch &l, const RowSums &r, int lane) {
@@ -138,7 +183,7 @@ __device__ __forceinline__ float row_loss(const VocabGeom<NR> &g, const DistillA
     const float lse = logf(r.s);
     float sum = 0.0f;
     for (int k = lane; k < a.k; k += 64) {
-        const float lq = ln_q(t, l.v[k]), q = expf(lq);
+        const float lq = ln_q_of_id(a, t, l, k), q = expf(ln_q(t, l.v[k]));
         const float lp = empty ? kNegInf : rel_ln(l.z[k], ref, g.inv_t) - lse;
         if (l.place[k] >= 0 && q != 0.0f) sum += q * (lq - lp);
     }
@@ -247,7 +292,7 @@ __device__ __forceinline__ void gradient_vec(const VocabGeom<NR> &g, const RowGr
     store_vec<DT>(grad_row_of<DT>(g, w.s, row), v, w, e0, held);
 }
 // The listed columns among the workgroup's tiles; an id's entries all store
-// the same, the difference from the sum of their probabilities.
+// the same.
 template <int DT, int NR>
 __device__ __forceinline__ void store_listed(const VocabGeom<NR> &g, const DistillArgs &a, const RowGradient &d,
                                              const Teacher &t, const ListScratch &l, long long row, int part) {
@@ -255,12 +300,7 @@ __device__ __forceinline__ void store_listed(const VocabGeom<NR> &g, const Disti
     each_entry(a, [&](int k) {
         const int place = l.place[k], waves = blockDim.x >> 6;
         if (place < 0 || place / kTileElems<DT> / waves % g.parts != part) return;
-        float q = expf(ln_q(t, l.v[k]));
-        if (count_entries(l, a.k, place) > 1) {
-            q = 0.0f;
-            for (int i = 0; i < a.k; ++i)
-                if (l.place[i] == place) q += expf(ln_q(t, l.v[i]));
-        }
+        const float q = expf(ln_q_of_id(a, t, l, k));
         const float p = d.total * exp2_fast(rel_log2(l.z[k], d.all, g.c) - d.lse2);
         store1<DT>(grad_row_of<DT>(g, l.s[k], row), l.e[k], round_to<DT>((p - q) * d.gs));
     });
@@ -288,7 +328,9 @@ __device__ __forceinline__ Stats listed_sums(const VocabGeom<NR> &g, const Disti
     each_entry(a, [&](int k) {
         const int place = l.place[k], waves = blockDim.x >> 6;
         if (place < 0 || place / kTileElems<DT> / waves % g.parts != part) return;
-        if (count_entries(l, k, place)) return;
+        bool first = true;
+        if (l.repeats) each_at(l, k, place, [&](int i) { first &= i >= k; });
+        if (!first) return;
         const float z = l.z[k];
         if (z > li.m) shift_stats(li, z, g.c);
         li.s += exp2_fast(rel(z, make_ref(li.m, g.c)));
@@ -340,8 +382,10 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
     Running run;
     Stats li{kNegInf, 0.0f, 0.0f};
     if (t.live) {                                              // a row without a teacher is not read further
+        note_repeats(a, list);
         Places places;
         if constexpr (TAIL) {
+            __syncthreads();
             places = load_places(list, a.k, lane);
             li = listed_sums<DT>(g, a, list, part);
         }
@@ -359,7 +403,10 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
     Stats st = total(run);
     block_sums<TAIL>(st, li, lds, waves, wave, lane, g.c);
     if (g.parts > 1) {
-        if (threadIdx.x == 0) a.part[row * g.parts + part] = make_float4(st.m, st.s, li.m, li.s);
+        // a sum's sign, which it does not need, says whether the list repeats an id
+        if (threadIdx.x == 0)
+            a.part[row * g.parts + part] =
+                make_float4(st.m, __builtin_copysignf(st.s, t.live && list.repeats ? -1.0f : 1.0f), li.m, li.s);
         return;
     }
     const RowSums r = join_sums(st, li, g.c);
@@ -385,8 +432,10 @@ __global__ __launch_bounds__(64 * kHeldWaves) void distill_held_kernel(const Voc
     const Teacher t = load_teacher<DT, TAIL>(g, a, list, row, lane);
     Stats st{kNegInf, 0.0f, 0.0f}, li = st;
     if (t.live) {
+        note_repeats(a, list);
         uint32_t bits[T];
         if constexpr (TAIL) {
+            __syncthreads();
             li = listed_sums<DT>(g, a, list, 0);
             const Places places = load_places(list, a.k, lane);
 #pragma unroll
@@ -423,11 +472,13 @@ __global__ __launch_bounds__(64) void distill_join_kernel(const VocabGeom<NR> g,
     Stats st{kNegInf, 0.0f, 0.0f}, li{kNegInf, 0.0f, 0.0f};
     if (lane < g.parts) {
         const float4 p = a.part[row * g.parts + lane];
-        st.m = p.x, st.s = p.y, li.m = p.z, li.s = p.w;
+        st.m = p.x, st.s = __builtin_fabsf(p.y), li.m = p.z, li.s = p.w;
+        if (lane == 0) list.repeats = f32_bits(p.y) >> 31;
     }
     wave_stats<false>(st, lane, g.c);
     wave_stats<false>(li, lane, g.c);
     const RowSums r = join_sums(st, li, g.c);
+    __syncthreads();
     const float loss = row_loss<TAIL>(g, a, t, list, r, lane);
     if (lane == 0) write_row(a, row, r, loss);
 }
@@ -440,6 +491,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_backward_kernel(cons
     const int local = blockIdx.x / g.parts, part = blockIdx.x - local * g.parts;
     const long long row = g.row0 + local;
     const Teacher t = load_teacher<DT, TAIL>(g, a, list, row, lane);
+    note_repeats(a, list);
     const float *o = a.saved + row * 4;
     const RowGradient d = row_gradient<DT, TAIL>(g, a, t, RowSums{o[0], o[1], o[2], o[3]}, row);
     gradient_tiles<DT>(g, a, d, t, list, row, part, part * waves + wave, step, lane);
@@ -447,17 +499,18 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_backward_kernel(cons
 
 template <int DT, int NR, bool TAIL>
 hipError_t run_distill(const VocabCall &c, const DistillArgs &a, VocabStage stage, hipStream_t s) {
+    const size_t lds = sizeof(int) << slot_bits(a.k);
     switch (stage) {
     case kForward:
-        if (c.again) return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, true>, c.parts, c.waves, s);
-        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, false>, c.parts, c.waves, s);
+        if (c.again) return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, true>, c.parts, c.waves, s, lds);
+        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, false, false>, c.parts, c.waves, s, lds);
     case kBoth:
-        if (c.held == 1) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 1>, 1, c.waves, s);
-        if (c.held == 2) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 2>, 1, c.waves, s);
-        if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s);
-        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true, true>, 1, c.waves, s);
-    case kBackward: return launch_rows<NR>(c, a, distill_backward_kernel<DT, NR, TAIL>, c.parts, c.waves, s);
-    default: return launch_rows<NR>(c, a, distill_join_kernel<DT, NR, TAIL>, 1, 1, s);
+        if (c.held == 1) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 1>, 1, c.waves, s, lds);
+        if (c.held == 2) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 2>, 1, c.waves, s, lds);
+        if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s, lds);
+        return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true, true>, 1, c.waves, s, lds);
+    case kBackward: return launch_rows<NR>(c, a, distill_backward_kernel<DT, NR, TAIL>, c.parts, c.waves, s, lds);
+    default: return launch_rows<NR>(c, a, distill_join_kernel<DT, NR, TAIL>, 1, 1, s, lds);
     }
 }
 

@@ -34,17 +34,18 @@ template <int NR> void fill_geom(const VocabCall &c, VocabGeom<NR> &g) {
     g.inv_t = (float)(1.0 / (double)c.temperature);
 }
 
-// One workgroup of ``waves`` waves for each of ``per_row`` parts of every row.
+// One workgroup of ``waves`` waves for each of ``per_row`` parts of every row,
+// with ``lds`` bytes beside what the kernel declares.
 template <int NR, typename A>
 hipError_t launch_rows(const VocabCall &c, const A &a, void (*k)(const VocabGeom<NR>, const A), int per_row, int waves,
-                       hipStream_t s) {
+                       hipStream_t s, size_t lds = 0) {
     VocabGeom<NR> g;
     fill_geom(c, g);
     const long long most = kVocabGridThreads / (64LL * waves * per_row);
     for (long long row = 0; row < c.rows; row += most) {
         g.row0 = row;
         const long long n = c.rows - row < most ? c.rows - row : most;
-        const hipError_t e = launch(k, dim3((unsigned)(n * per_row)), dim3(64u * (unsigned)waves), 0, s, g, a);
+        const hipError_t e = launch(k, dim3((unsigned)(n * per_row)), dim3(64u * (unsigned)waves), lds, s, g, a);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
