@@ -422,6 +422,18 @@ def vocab_widths(vocab, n):
     return [(r + 1) * vocab // n - r * vocab // n for r in range(n)]
 
 
+def _at_pitch(b, pitch, rows):
+    """Whether a tensor's rows (all its dimensions but the last) are packed elements ``pitch`` apart."""
+    if b.dim() == 0 or b.numel() == 0 or (b.dim() != 2 and b.is_contiguous()):
+        return True
+    outer = [(size, stride) for size, stride in zip(b.shape[:-1], b.stride()[:-1]) if size > 1]
+    if b.shape[-1] > 1 and b.stride(-1) != 1:
+        return False
+    if any(a[1] != c[0] * c[1] for a, c in zip(outer, outer[1:])):
+        return False
+    return not outer or outer[-1][1] == pitch or rows <= 1
+
+
 def _logit_table(bufs, shape, grads=False):
     """Pointer table of rank buffers; tensors must have the shape's type and hold its rows."""
     if not isinstance(bufs, PointerTable):
@@ -438,8 +450,7 @@ def _logit_table(bufs, shape, grads=False):
             if shape.rows and w and room < (shape.rows - 1) * p + w:
                 raise ValueError("rank buffer holds %d elements; %d rows of %d at pitch %d need more"
                                  % (room, shape.rows, w, p))
-            if b.dim() == 2 and b.shape[0] > 1 and b.shape[1] > 0 and (b.stride(1) != 1 and b.shape[1] > 1
-                                                                       or b.stride(0) != p and shape.rows > 1):
+            if not _at_pitch(b, p, shape.rows):
                 raise ValueError("rank buffer has strides %s; its pitch is %d" % (tuple(b.stride()), p))
         bufs._checked = (shape, grads)
     return bufs.array
