@@ -434,7 +434,18 @@ def _at_pitch(b, pitch, rows):
     return not outer or outer[-1][1] == pitch or rows <= 1
 
 
-def _logit_table(bufs, shape, grads=False):
+def _on_host(t):
+    """Whether a tensor lies where no kernel can reach it (pinned memory can be reached)."""
+    return not t.is_cuda and t.numel() > 0 and not t.is_pinned()
+
+
+def _refuse(host, shape):
+    """Refuse tensors in host memory by name, once all else about the arguments is right."""
+    if host and shape.rows:
+        raise ValueError("%s must be on the GPU, not in host memory" % host[0])
+
+
+def _logit_table(bufs, shape, host, grads=False):
     """Pointer table of rank buffers; tensors must have the shape's type and hold its rows."""
     if not isinstance(bufs, PointerTable):
         bufs = PointerTable(bufs)
@@ -452,30 +463,38 @@ def _logit_table(bufs, shape, grads=False):
                                  % (room, shape.rows, w, p))
             if not _at_pitch(b, p, shape.rows):
                 raise ValueError("rank buffer has strides %s; its pitch is %d" % (tuple(b.stride()), p))
-        bufs._checked = (shape, grads)
+            if _on_host(b):
+                host.append("grads" if grads else "logits")
+        if not host:
+            bufs._checked = (shape, grads)
     return bufs.array
 
 
-def _vector(t, dtype, numel, what):
-    """Address of a contiguous tensor argument (integer addresses and None pass through)."""
+def _vector(t, dtype, numel, what, host):
+    """Address of a contiguous tensor argument (integer addresses and None pass through); its name goes into ``host``
+    if it is in host memory."""
     if t is None or isinstance(t, int):
         return t
     if str(t.dtype) != dtype or t.numel() < numel or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of at least %d elements" % (what, dtype, numel))
+    if _on_host(t):
+        host.append(what)
     return t.data_ptr()
 
 
-def _f32(t, numel, what):
-    return _vector(t, "torch.float32", numel, what)
+def _f32(t, numel, what, host):
+    return _vector(t, "torch.float32", numel, what, host)
 
 
-def _i64(t, numel, what):
-    return _vector(t, "torch.int64", numel, what)
+def _i64(t, numel, what, host):
+    return _vector(t, "torch.int64", numel, what, host)
 
 
-def _workspace(w):
+def _workspace(w, host):
     if w is None:
         return None, 0
+    if _on_host(w):
+        host.append("workspace")
     return w.data_ptr() or None, w.numel() * w.element_size()
 
 
@@ -490,39 +509,46 @@ def ar_logprobs(logits, shape, targets, logprobs, entropy=None, top_k=0, top_log
                 workspace=None, stream=None):
     """ln p of each row's target; optionally the entropy, the ``top_k`` most
     likely entries, and the statistics ``ar_logprobs_backward`` needs."""
-    r, (ws, wb) = shape.rows, _workspace(workspace)
-    _check(_lib.ar_logprobs(_logit_table(logits, shape), shape.ref, _i64(targets, r, "targets"),
-                            _f32(logprobs, r, "logprobs"), _f32(entropy, r, "entropy"), top_k,
-                            _f32(top_logprobs, r * top_k, "top_logprobs"), _i64(top_ids, r * top_k, "top_ids"),
-                            _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+    r, host = shape.rows, []
+    ws, wb = _workspace(workspace, host)
+    args = (_logit_table(logits, shape, host), shape.ref, _i64(targets, r, "targets", host),
+            _f32(logprobs, r, "logprobs", host), _f32(entropy, r, "entropy", host), top_k,
+            _f32(top_logprobs, r * top_k, "top_logprobs", host), _i64(top_ids, r * top_k, "top_ids", host),
+            _f32(saved, 4 * r, "saved", host))
+    _refuse(host, shape)
+    _check(_lib.ar_logprobs(*args, ws, wb, _stream(stream)))
 
 
 def ar_logprobs_backward(logits, grads, shape, targets, saved, grad_logprobs=None, grad_entropy=None, stream=None):
     """Gradient of the logits from the gradients of the log probabilities and entropies."""
-    r = shape.rows
-    _check(_lib.ar_logprobs_backward(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref,
-                                     _i64(targets, r, "targets"), _f32(saved, 4 * r, "saved"),
-                                     _f32(grad_logprobs, r, "grad_logprobs"), _f32(grad_entropy, r, "grad_entropy"),
-                                     _stream(stream)))
+    r, host = shape.rows, []
+    args = (_logit_table(logits, shape, host), _logit_table(grads, shape, host, True), shape.ref,
+            _i64(targets, r, "targets", host), _f32(saved, 4 * r, "saved", host),
+            _f32(grad_logprobs, r, "grad_logprobs", host), _f32(grad_entropy, r, "grad_entropy", host))
+    _refuse(host, shape)
+    _check(_lib.ar_logprobs_backward(*args, _stream(stream)))
 
 
 def ar_logprobs_grad(logits, grads, shape, targets, logprobs=None, grad_logprobs=None, grad_entropy=None,
                      entropy=None, saved=None, workspace=None, stream=None):
     """Log probabilities (optionally entropies) and the gradient in one call."""
-    r, (ws, wb) = shape.rows, _workspace(workspace)
-    _check(_lib.ar_logprobs_grad(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref,
-                                 _i64(targets, r, "targets"), _f32(grad_logprobs, r, "grad_logprobs"),
-                                 _f32(grad_entropy, r, "grad_entropy"), _f32(logprobs, r, "logprobs"),
-                                 _f32(entropy, r, "entropy"), _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+    r, host = shape.rows, []
+    ws, wb = _workspace(workspace, host)
+    args = (_logit_table(logits, shape, host), _logit_table(grads, shape, host, True), shape.ref,
+            _i64(targets, r, "targets", host), _f32(grad_logprobs, r, "grad_logprobs", host),
+            _f32(grad_entropy, r, "grad_entropy", host), _f32(logprobs, r, "logprobs", host),
+            _f32(entropy, r, "entropy", host), _f32(saved, 4 * r, "saved", host))
+    _refuse(host, shape)
+    _check(_lib.ar_logprobs_grad(*args, ws, wb, _stream(stream)))
 
 
-def _teacher(shape, ids, values, k):
+def _teacher(shape, ids, values, k, host):
     """(k, ids address, values address): k from a two-dimensional list of ids unless given."""
     if k is None:
         if ids is None or isinstance(ids, int) or ids.dim() != 2:
             raise ValueError("k is needed unless teacher_ids is a two-dimensional tensor")
         k = ids.shape[1]
-    return k, _i64(ids, shape.rows * k, "teacher_ids"), _f32(values, shape.rows * k, "teacher_values")
+    return k, _i64(ids, shape.rows * k, "teacher_ids", host), _f32(values, shape.rows * k, "teacher_values", host)
 
 
 def ar_distill(logits, shape, teacher_ids, teacher_values, loss, tail=False, k=None, saved=None, workspace=None,
@@ -530,27 +556,34 @@ def ar_distill(logits, shape, teacher_ids, teacher_values, loss, tail=False, k=N
     """Divergence of the student's distribution from a teacher's top entries
     (``tail``: log probabilities with the remaining mass compared as well;
     otherwise renormalised logits)."""
-    r, (ws, wb) = shape.rows, _workspace(workspace)
-    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
-    _check(_lib.ar_distill(_logit_table(logits, shape), shape.ref, ids, values, k, int(bool(tail)),
-                           _f32(loss, r, "loss"), _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+    r, host = shape.rows, []
+    ws, wb = _workspace(workspace, host)
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k, host)
+    args = (_logit_table(logits, shape, host), shape.ref, ids, values, k, int(bool(tail)), _f32(loss, r, "loss", host),
+            _f32(saved, 4 * r, "saved", host))
+    _refuse(host, shape)
+    _check(_lib.ar_distill(*args, ws, wb, _stream(stream)))
 
 
 def ar_distill_backward(logits, grads, shape, teacher_ids, teacher_values, saved, tail=False, k=None, grad_loss=None,
                         stream=None):
     """Gradient of the logits from the gradients of the rows' losses (None: ones)."""
-    r = shape.rows
-    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
-    _check(_lib.ar_distill_backward(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref, ids,
-                                    values, k, int(bool(tail)), _f32(saved, 4 * r, "saved"),
-                                    _f32(grad_loss, r, "grad_loss"), _stream(stream)))
+    r, host = shape.rows, []
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k, host)
+    args = (_logit_table(logits, shape, host), _logit_table(grads, shape, host, True), shape.ref, ids, values, k,
+            int(bool(tail)), _f32(saved, 4 * r, "saved", host), _f32(grad_loss, r, "grad_loss", host))
+    _refuse(host, shape)
+    _check(_lib.ar_distill_backward(*args, _stream(stream)))
 
 
 def ar_distill_grad(logits, grads, shape, teacher_ids, teacher_values, loss=None, tail=False, k=None, grad_loss=None,
                     saved=None, workspace=None, stream=None):
     """The rows' losses and the gradient in one call."""
-    r, (ws, wb) = shape.rows, _workspace(workspace)
-    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k)
-    _check(_lib.ar_distill_grad(_logit_table(logits, shape), _logit_table(grads, shape, True), shape.ref, ids, values,
-                                k, int(bool(tail)), _f32(grad_loss, r, "grad_loss"), _f32(loss, r, "loss"),
-                                _f32(saved, 4 * r, "saved"), ws, wb, _stream(stream)))
+    r, host = shape.rows, []
+    ws, wb = _workspace(workspace, host)
+    k, ids, values = _teacher(shape, teacher_ids, teacher_values, k, host)
+    args = (_logit_table(logits, shape, host), _logit_table(grads, shape, host, True), shape.ref, ids, values, k,
+            int(bool(tail)), _f32(grad_loss, r, "grad_loss", host), _f32(loss, r, "loss", host),
+            _f32(saved, 4 * r, "saved", host))
+    _refuse(host, shape)
+    _check(_lib.ar_distill_grad(*args, ws, wb, _stream(stream)))

@@ -10,7 +10,7 @@ from reduce_scatter_amd import _binding as b  # noqa: E402
 
 
 def check(t, rows, width, pitch):
-    return b._logit_table([t], ar.VocabShape(rows, [width], "f32", pitches=[pitch]))
+    return b._logit_table([t], ar.VocabShape(rows, [width], "f32", pitches=[pitch]), [])
 
 
 def test_rows_that_no_pitch_describes():
