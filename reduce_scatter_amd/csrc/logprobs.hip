@@ -413,6 +413,8 @@ hipError_t run_logprobs(const VocabCall &c, const LogprobsArgs &a, VocabStage st
                   : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, false, true, true>, 1, c.waves, s);
     }
     if (stage == kForward) {
+        if (top && c.again)
+            return launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false, true>, c.parts, c.waves, s);
         if (top) return s1 ? launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, true, false, false>, c.parts, c.waves, s)
                            : launch_rows<NR>(c, a, logprobs_kernel<DT, NR, false, true, false, false>, c.parts, c.waves, s);
         if (c.again) return launch_rows<NR>(c, a, logprobs_kernel<DT, NR, true, false, false, true>, c.parts, c.waves, s);

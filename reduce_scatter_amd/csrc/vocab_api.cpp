@@ -111,9 +111,12 @@ VocabCall both_rows(const Shape &s, int most) {
 }
 
 // Whether a forward call that saves statistics for a backward one should leave
-// the logits in the 256 MB Infinity Cache: where they fit.  Measured with
-// (without) on 2000 x 32000 fp32, 256 MB: 138 (160) us for both calls; past it
-// non-temporal loads read 7.0 TB/s, plain ones 6.0-6.5.
+// the logits in the 256 MB Infinity Cache: where they fit.  Both calls together
+// with (without), us, after the logits were written: 2000 x 32000 fp32 135 (152),
+// with 20 alternatives 157 (173); bf16 4000 x 32000 144 (163), 500 x 131072 73
+// (78), with 5 alternatives 84 (90), 64 x 131072 20 (24).  Where the cache is
+// full of other data that has yet to be written back, they lose it: 4000 x 32000 177
+// (165).  Past 256 MB non-temporal loads read 7.0 TB/s, plain ones 6.0-6.5.
 bool read_again(const Shape &s, const float *saved) {
     const double bytes = (double)s.c.rows * s.vocab * (s.c.dtype == AR_FLOAT32 ? 4 : 2);
     return saved && bytes <= 256.0 * (1 << 20);
