@@ -507,7 +507,8 @@ hipError_t run_distill(const VocabCall &c, const DistillArgs &a, VocabStage stag
     case kBoth:
         if (c.held == 1) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 1>, 1, c.waves, s, lds);
         if (c.held == 2) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, 2>, 1, c.waves, s, lds);
-        if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s, lds);
+        if constexpr (!TAIL || DT == BF16)                     // the others are never chosen (vocab_api.cpp)
+            if (c.held) return launch_rows<NR>(c, a, distill_held_kernel<DT, NR, TAIL, kHeldTiles>, 1, c.waves, s, lds);
         return launch_rows<NR>(c, a, distill_kernel<DT, NR, TAIL, true, true>, 1, c.waves, s, lds);
     case kBackward: return launch_rows<NR>(c, a, distill_backward_kernel<DT, NR, TAIL>, c.parts, c.waves, s, lds);
     default: return launch_rows<NR>(c, a, distill_join_kernel<DT, NR, TAIL>, 1, 1, s, lds);

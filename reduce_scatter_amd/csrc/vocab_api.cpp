@@ -89,25 +89,51 @@ VocabCall short_rows(const Shape &s) {
 
 // Results and gradient in one launch: the row stays in registers where it
 // fits into 16 waves of four tiles (131072 columns of 16-bit logits, half that
-// in fp32): few rows take as few tiles a wave as they can, many rows four, if
-// `most` waves suffice and they fill most of the 16 that a compute unit then
-// holds.  Elsewhere the row is read twice.  Registers (reading twice), us:
-// cross-entropy 8192 x 32768 bf16 200 (233), 4096 x 131072 410 (473),
-// 8192 x 32768 fp32 388 (453); distillation with a tail 8192 x 32768 232 (274),
-// but 4096 x 131072, 16 waves of one row: 503 (475), and 8192 x 32768 fp32: 514
-// (471); cross-entropy 4096 x 100003, where 13 of the 16 waves are filled: 387 (379).
-VocabCall both_rows(const Shape &s, int most) {
+// in fp32), elsewhere it is read twice.  A compute unit holds 16 such waves,
+// four to each of its SIMDs, so with many rows it depends on the number of
+// waves W of a row what that gives.  Time in registers over time reading
+// twice, rows of 1/2 GB at 16-byte boundaries / of an odd length in four ranks:
+//            bf16                          fp32
+//   W        cross     entropy   tail      cross     list      tail
+//   2        .84/.70   .93/.84   .88/.71   .86/.73   .86/.71  1.19/.86
+//   4        .88/.81   .95/.93   .83/.81   .90/.84   .86/.81  1.12/1.06
+//   5        .90/1.09 1.14/1.36 1.27/1.53  .87/.85   .98/1.07 1.49/1.55
+//   7        .80/.85   .97/1.06 1.00/1.07  .81/.83   .86/.90  1.22/1.26
+//   8        .79/.82   .92/.96   .85/.89   .79/.83   .83/.87  1.11/1.12
+//   9        .94/1.09 1.15/1.34 1.31/1.52  .85/.92   .98/1.10 1.33/1.44
+//   10       .92/1.00 1.13/1.24 1.30/1.41  .83/.89   .99/1.05 1.33/1.37
+//   12       .85/.90  1.03/1.11 1.12/1.21  .82/.87   .91/.97  1.24/1.28
+//   13       .85/1.05 1.04/1.28 1.17/1.37  .82/.88   .90/1.03 1.21/1.29
+//   16       .83/.91  1.00/1.12 1.03/1.14  .83/.89   .87/.93  1.20/1.23
+// (a list without a tail in bf16 about as entropy; fp16 as bf16, but for a
+// tail, where its kernel runs out of registers as fp32's does: 1.12-1.86.)
+enum class Hold {
+    never,
+    pairs,                             // where two rows or more fill 7/8 of a compute unit
+    even,                              // not where one SIMD has a wave more than all others, nor where six waves idle
+    always
+};
+Hold hold_rule(int dtype, bool weighted, bool list, bool tail) {
+    if (tail) return dtype == AR_BFLOAT16 ? Hold::pairs : Hold::never;
+    if (dtype == AR_FLOAT32) return list ? Hold::even : Hold::always;
+    return list || weighted ? Hold::pairs : Hold::even;
+}
+
+// Few rows, a compute unit to each, take as few tiles a wave as they can, to be
+// done sooner: 256 x 65280 bf16 (two tiles) cross-entropy 15.3 us (reading twice
+// 17.9), with a tail 20.9 (23.1), 200 x 32512 fp32 17.2 (20.9), 16 x 32512 bf16 9.3
+// (9.1); with 10 to 14 waves up to 1.2 times slower: 128 x 40704 with a tail 16.3
+// (14.1).  Four tiles and a tail, as above: 200 x 52992 fp32 29.5 (24.7).
+VocabCall both_rows(const Shape &s, Hold hold) {
     VocabCall c = s.c;
-    int held = kHeldTiles;
-    if (c.rows <= 256) {
-        held = c.tiles <= kHeldWaves ? 1 : c.tiles <= 2 * kHeldWaves ? 2 : kHeldTiles;
-        most = kHeldWaves;
-    }
-    const int waves = (c.tiles + held - 1) / held;
-    if (waves > most || (c.rows > 256 && kHeldWaves / waves * waves < 14)) return short_rows(s);
-    c.held = held;
-    c.waves = waves;
-    return c;
+    const bool few = c.rows <= 256;
+    c.held = !few || c.tiles > 2 * kHeldWaves ? kHeldTiles : c.tiles > kHeldWaves ? 2 : 1;
+    c.waves = (c.tiles + c.held - 1) / c.held;
+    const int w = c.waves;
+    const bool pays = few ? c.held < kHeldTiles || hold != Hold::never
+                          : hold == Hold::always || (hold == Hold::even && (w == 1 || (w % 4 != 1 && w != 10))) ||
+                                (hold == Hold::pairs && (w <= 4 || w == 7 || w == 8));
+    return pays && w <= kHeldWaves ? c : short_rows(s);
 }
 
 // Whether a forward call that saves statistics for a backward one should leave
@@ -322,7 +348,10 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
     a.saved = saved;
     a.grad_logprobs = grad_logprobs;
     a.grad_entropy = grad_entropy;
-    if (s.c.parts == 1) return hip_status(launch_logprobs(both_rows(s, kHeldWaves), a, kBoth, stream));
+    if (s.c.parts == 1) {
+        const Hold hold = hold_rule(s.c.dtype, entropy || saved || grad_entropy, false, false);
+        return hip_status(launch_logprobs(both_rows(s, hold), a, kBoth, stream));
+    }
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     s.c.again = read_again(s, a.saved);
@@ -409,8 +438,8 @@ ar_status_t ar_distill_grad(const void *const *logits, void *const *grads, const
     a.saved = saved;
     a.grad_loss = grad_loss;
     const bool tail = mode == AR_TEACHER_TAIL;
-    const int most = !tail ? kHeldWaves : s.c.dtype == AR_FLOAT32 ? 0 : kHeldWaves / 2;       // see both_rows
-    if (s.c.parts == 1) return hip_status(launch_distill(both_rows(s, most), a, tail, kBoth, stream));
+    if (s.c.parts == 1)
+        return hip_status(launch_distill(both_rows(s, hold_rule(s.c.dtype, false, true, tail)), a, tail, kBoth, stream));
     a.part = (float4 *)((char *)workspace + w.part);
     if (!a.saved) a.saved = (float *)((char *)workspace + w.saved);
     s.c.again = read_again(s, a.saved);
