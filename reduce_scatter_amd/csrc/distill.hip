@@ -364,9 +364,10 @@ __device__ __forceinline__ void block_sums(Stats &st, Stats &li, SumScratch &lds
 // with BOTH its gradient by the same workgroup.  AGAIN: the logits will be
 // read again soon and are left in the caches.
 // Bound by HBM where rows are many: with BOTH 8192 x 131072 bf16, 64 entries
-// and a tail 910 us, 7.0 TB/s for two reads and one write.  Of 777 x 50021
-// with 100 entries, three rows to a compute unit, the list and the joining
-// are most (45 us; the bytes take 11).
+// and a tail 909 us, 7.0 TB/s for two reads and one write.  With fewer it goes
+// by rounds: scalar registers allow seven waves to a SIMD, three workgroups to
+// a compute unit, 768 rows at once.  With 100 entries 768 x 50021 bf16 take 34
+// us, 780 rows 41 (the bytes 11): list, stream and joining once more.
 template <int DT, int NR, bool TAIL, bool BOTH, bool AGAIN>
 __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGeom<NR> g, const DistillArgs a) {
     __shared__ SumScratch lds;
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(64 * kVocabWaves) void distill_kernel(const VocabGe
 }
 
 // Loss and gradient of a row held in the workgroup's registers: 8192 x 32768
-// bf16, 64 entries and a tail 232 us (read twice: 274).
+// bf16, 64 entries and a tail 229 us (read twice: 257).
 template <int DT, int NR, bool TAIL, int T>
 __global__ __launch_bounds__(64 * kHeldWaves) void distill_held_kernel(const VocabGeom<NR> g, const DistillArgs a) {
     __shared__ SumScratch lds;

@@ -60,14 +60,14 @@ ar_status_t check_shape(const ar_vocab_t *v, Shape &s) {
     // Waves per row, at most one to a tile.  A wave pays about 2 us of set-up
     // and merging per row, so waves are only added while rows * waves leaves
     // compute units short of work; measured on 8192 x 131072 bf16 (us) with 1,
-    // 2, 4, 8 waves: 330, 336, 346, 375; on 777 x 50021: 168, 114, 94, 97.
+    // 2, 4, 8 waves: 329, 326, 325, 338; on 777 x 50021: 38, 27, 29, 27.
     int waves = 1;
     while (waves < kVocabWaves && waves * 2 <= tiles && v->rows * waves < 16384) waves *= 2;
     // Workgroups per row, while the rows alone leave compute units idle and
     // every wave keeps two tiles; joining them is a second launch (about 4 us),
     // so not below five tiles a wave: 64 x 131072 bf16 with 20 alternatives
-    // (us) in 1, 2, 4, 8 workgroups: 22.5, 22.1, 19.1, 22.9; one row of 32768: 11.0,
-    // 13.7, 13.7, 13.6; a distillation step on 16 x 32768 fp32: 13.3, 17.9, 16.9, 16.7.
+    // (us) in 1, 2, 4, 8 workgroups: 19.9, 20.1, 18.5, 21.6; one row of 32768 in 1,
+    // 2, 4: 10.5, 13.4, 13.7; a distillation step on 16 x 32768 fp32: 13.2, 19.2, 17.4.
     int parts = 1;
     while (tiles > 4 * waves && parts < kVocabParts && parts * 4 * waves <= tiles && v->rows * parts * 2 <= 256)
         parts *= 2;
@@ -80,7 +80,7 @@ ar_status_t check_shape(const ar_vocab_t *v, Shape &s) {
 // gradient in the same call, its top entries): as many waves as there may be,
 // so that few rows are in flight and the second look finds them in the caches.
 // Measured on 8192 x 131072 bf16 (distillation step, us) with 1, 2, 4, 8
-// waves: 1250, 1192, 931, 920; on 512 x 131072 (top 64): 1064, 336, 149, 85.
+// waves: 1239, 1167, 931, 931; on 512 x 131072 (top 64): 552, 100, 55, 47.
 VocabCall short_rows(const Shape &s) {
     VocabCall c = s.c;
     while (c.waves < kVocabWaves && c.waves * 2 <= c.tiles && c.parts == 1) c.waves *= 2;
