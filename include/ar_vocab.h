@@ -122,7 +122,8 @@ ar_status_t ar_logprobs_grad(const void *const *logits, void *const *grads, cons
 /* ``teacher_ids`` [rows, k] int64, ``teacher_values`` [rows, k] fp32,
  * 1 <= k <= AR_TEACHER_MAX; ``loss`` [rows] fp32; optional ``saved``
  * [rows, 4] fp32 for ar_distill_backward: m and the sum as above, and the same
- * two of the unlisted entries alone (AR_TEACHER_RENORM: of all entries again). */
+ * two of the unlisted entries alone (AR_TEACHER_RENORM: of all entries again);
+ * -inf and 0 in a row without a teacher, whose logits are not summed. */
 ar_status_t ar_distill(const void *const *logits, const ar_vocab_t *shape, const int64_t *teacher_ids,
                        const float *teacher_values, int k, ar_teacher_t mode, float *loss, float *saved,
                        void *workspace, size_t workspace_bytes, hipStream_t stream);

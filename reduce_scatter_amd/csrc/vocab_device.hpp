@@ -403,7 +403,7 @@ __device__ __forceinline__ Place place_of(const VocabGeom<NR> &g, long long row,
 
 // t and 2^t of a logit for its gradient.  In units of log2 a logit far below
 // the reference carries |t| 2^-24 of rounding into 2^t.  In the sums that
-// averages out, and gradients of 16-bit logits are rounded to 2^-9 or 2^-12,
+// averages out, and gradients of 16-bit logits are rounded to 2^-8 or 2^-11,
 // so these take t relative to y (term_shift() of the reference off); for
 // those of fp32 the product (x - m) c is carried in two parts (c too), which
 // leaves the rounding of x - m itself.  Where x - m overflows the low

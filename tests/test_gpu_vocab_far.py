@@ -46,10 +46,10 @@ def test_masks_of_any_finite_value(dtype, fill, temperature, rows, widths):
     check_all_calls(d, best, 9, gl, gh, ids, vals)
 
 
-@pytest.mark.parametrize("temperature", [1e-4, 1e-9, 1e-20])
+@pytest.mark.parametrize("temperature", [1e-4, 1e-9, 1e-20, 1e-30, 1e30])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-def test_temperatures_near_zero(dtype, temperature):
-    """Ordinary logits far apart in units of the temperature: the largest takes all."""
+def test_extreme_temperatures(dtype, temperature):
+    """Ordinary logits far apart in units of the temperature, where the largest takes all; or all but equal."""
     rng = np.random.default_rng(32)
     rows, vocab = 6, 3001
     x = base.logits(rng, rows, vocab)
