@@ -19,7 +19,8 @@ constexpr int kPer = kTeacherMax / 64;             // entries per lane, where a 
 
 // A row's list in LDS.
 struct ListScratch {
-    alignas(16) int place[kTeacherMax];            // tile * kTileElems + element there (-1: padding, also to a multiple of 4)
+    alignas(16) int place[kTeacherMax];            // tile * kTileElems + element there; -1: padding, also to a
+                                                   // multiple of 4 entries
     int s[kTeacherMax], e[kTeacherMax];            // rank and element there
     float v[kTeacherMax];                          // the teacher's value
     float z[kTeacherMax];                          // the student's logit, read before any gradient is stored

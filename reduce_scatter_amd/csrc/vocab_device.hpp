@@ -8,10 +8,10 @@
 // logit and 2^t one instruction; the rounding of y is the same for every
 // logit, so sums stand against y as they are joined, and a row's whole sums are
 // taken to m itself (settled) before any result or gradient uses them.  The
-// reference need not be the maximum: a lane takes
-// its first vector's and keeps it while a tile's sum stays below 2^16, so the
-// stream takes no maxima; a vector that carries the sum past that is added again after moving
-// the reference.
+// reference need not be the maximum: a lane takes its first vector's and keeps
+// it while a tile's sum stays below 2^16, so the stream takes no maxima; a
+// vector that carries the sum past that is added again after moving the
+// reference.
 #pragma once
 
 #include "ar_device.hpp"
@@ -32,13 +32,13 @@ __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __
 
 // The reference of a set of logits: t = x*c - y.  m = -inf (nothing but masked
 // logits) counts from 0.  For x = m that leaves t = residue(), what rounding y
-// took away: up to half a unit in the last place of m*c.  That is no more than 32 while
-// |m*c| is below 2^30, but hundreds and more beyond (masks of -1e10, or any
-// logit at a temperature near 0), infinity or zero to 2^t.  From 2^30 on c
-// therefore is the power of two that puts |m| c into [2^30, 2^31): the product is
-// exact, t = 0 at x = m, and any other number is a unit in m's last place
-// away, 2^6 at least in t under either scale, where 2^t counts for nothing
-// beside 1 (2^20 columns of it are 2^-44).
+// took away: up to half a unit in the last place of m*c.  That is no more than
+// 32 while |m*c| is below 2^30, but hundreds and more beyond (masks of -1e10,
+// or any logit at a temperature near 0), infinity or zero to 2^t.  From 2^30 on
+// c therefore is the power of two that puts |m| c into [2^30, 2^31): the
+// product is exact, t = 0 at x = m, and any other number is a unit in m's last
+// place away, 2^6 at least in t under either scale, where 2^t counts for
+// nothing beside 1 (2^20 columns of it are 2^-44).
 struct Ref {
     float m, y, c;
     bool wide;                         // c is that power of two instead of log2(e) / T
@@ -89,7 +89,8 @@ __device__ __forceinline__ void shift_by(Stats &a, float to, float d, float f) {
 // ref_shift without making the references, unless some lane's is wide.
 __device__ __forceinline__ void shift_stats(Stats &a, float to, float c) {
     const float from_y = a.m * c, to_y = to * c;
-    const bool wide = (finite(a.m) && __builtin_fabsf(from_y) >= kWide) || (finite(to) && __builtin_fabsf(to_y) >= kWide);
+    const bool wide = (finite(a.m) && __builtin_fabsf(from_y) >= kWide) ||
+                      (finite(to) && __builtin_fabsf(to_y) >= kWide);
     float d = a.m == to ? 0.0f : from_y - to_y;
     if (__builtin_expect(__any(wide), 0)) d = ref_shift(make_ref(a.m, c), make_ref(to, c), c);
     shift_by(a, to, d, exp2_fast(d));
