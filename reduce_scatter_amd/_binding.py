@@ -587,3 +587,298 @@ def ar_distill_grad(logits, grads, shape, teacher_ids, teacher_values, loss=None
             _f32(saved, 4 * r, "saved", host))
     _refuse(host, shape)
     _check(_lib.ar_distill_grad(*args, ws, wb, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators around a step's collectives (include/ar_layer.h)
+# ---------------------------------------------------------------------------
+
+class _NormStruct(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("rows", ctypes.c_longlong), ("width", ctypes.c_longlong), ("pitches", ctypes.POINTER(ctypes.c_longlong)),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float), ("group", ctypes.c_int)]
+
+
+class _EmbedStruct(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("tokens", ctypes.c_longlong), ("width", ctypes.c_longlong),
+                ("entries", ctypes.POINTER(ctypes.c_longlong)), ("pitches", ctypes.POINTER(ctypes.c_longlong)),
+                ("grad_pitches", ctypes.POINTER(ctypes.c_longlong)), ("scale", ctypes.c_float)]
+
+
+class _GradsStruct(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_longlong), ("bufs", ctypes.c_void_p), ("sizes", ctypes.POINTER(ctypes.c_longlong)),
+                ("dtypes", ctypes.POINTER(ctypes.c_int))]
+
+
+_szp, _float = ctypes.POINTER(ctypes.c_size_t), ctypes.c_float
+_nshape, _eshape, _glist = ctypes.POINTER(_NormStruct), ctypes.POINTER(_EmbedStruct), ctypes.POINTER(_GradsStruct)
+_lib.ar_reduce_norm.argtypes = [_vpp, _nshape, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.ar_norm_workspace.argtypes = [_nshape, _szp]
+_lib.ar_reduce_norm_backward.argtypes = [_vp, ctypes.c_longlong, _nshape, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         ctypes.c_size_t, _vp]
+_lib.ar_embedding.argtypes = [_vpp, _eshape, _vp, _vp, _vp]
+_lib.ar_embedding_workspace.argtypes = [_eshape, _szp]
+_lib.ar_embedding_backward.argtypes = [_vp, _eshape, _vp, _vpp, _int, _vp, ctypes.c_size_t, _vp]
+_lib.ar_grad_workspace.argtypes = [_glist, _szp]
+_lib.ar_grad_norm.argtypes = [_glist, _float, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.ar_clip_grads.argtypes = [_glist, _vpp, _float, _float, _float, _vp, _vp, ctypes.c_size_t, _vp]
+for _f in (_lib.ar_reduce_norm, _lib.ar_norm_workspace, _lib.ar_reduce_norm_backward, _lib.ar_embedding,
+           _lib.ar_embedding_workspace, _lib.ar_embedding_backward, _lib.ar_grad_workspace, _lib.ar_grad_norm,
+           _lib.ar_clip_grads):
+    _f.restype = ctypes.c_int
+
+_TYPES = {DTYPES["f32"]: "torch.float32", DTYPES["bf16"]: "torch.bfloat16", DTYPES["f16"]: "torch.float16"}
+_BYTES = ("torch.float8_e4m3fn", "torch.uint8")
+
+
+def _longs(values, n, what):
+    if values is not None and len(values) != n:
+        raise ValueError("one %s per rank" % what)
+    return None if values is None else (ctypes.c_longlong * max(1, n))(*[int(v) for v in values])
+
+
+class NormShape:
+    """Rows of ``width`` columns whose sum over n rank buffers is normalised:
+    rows of rank r ``pitches[r]`` elements apart (default: the width), the
+    weight in ``weight_dtype`` (default: the rows' type; else fp32) around
+    ``offset``, and ``group`` columns to a scale of the 8-bit output (0: the
+    row).  Built once and reusable across calls."""
+
+    def __init__(self, rows, width, n, dtype, pitches=None, weight_dtype=None, eps=1e-6, offset=0.0, group=0):
+        self.rows, self.width, self.n = int(rows), int(width), int(n)
+        self.dtype = _dtype_code(dtype)
+        self.weight_dtype = self.dtype if weight_dtype is None else _dtype_code(weight_dtype)
+        self.eps, self.offset, self.group = float(eps), float(offset), int(group)
+        self.pitches = [self.width] * self.n if pitches is None else [int(p) for p in pitches]
+        self._pitches = _longs(self.pitches, self.n, "pitch")
+        self.groups = -(-self.width // self.group) if self.group > 0 else 1
+        self._struct = _NormStruct(self.n, self.dtype, self.weight_dtype, self.rows, self.width, self._pitches, self.eps,
+                                   self.offset, self.group)
+        self.ref = ctypes.byref(self._struct)
+
+
+class EmbedShape:
+    """``tokens`` rows of ``width`` columns looked up in a table of which rank r
+    holds ``entries[r]`` rows, ``pitches[r]`` elements apart (default: the
+    width), its gradient's ``grad_pitches[r]`` (default: the pitches).
+    ``dtype`` is the table's and its gradient's type, ``out_dtype`` that of the
+    looked-up rows and their gradient (default: the same).  Built once and
+    reusable across calls."""
+
+    def __init__(self, tokens, entries, width, dtype, out_dtype=None, pitches=None, grad_pitches=None, scale=1.0):
+        self.tokens, self.entries, self.n, self.width = int(tokens), [int(e) for e in entries], len(entries), int(width)
+        self.dtype = _dtype_code(dtype)
+        self.out_dtype = self.dtype if out_dtype is None else _dtype_code(out_dtype)
+        self.pitches = [self.width] * self.n if pitches is None else [int(p) for p in pitches]
+        self.grad_pitches = self.pitches if grad_pitches is None else [int(p) for p in grad_pitches]
+        self.scale = float(scale)
+        self._arrays = (_longs(self.entries, self.n, "entry"), _longs(self.pitches, self.n, "pitch"),
+                        _longs(self.grad_pitches, self.n, "pitch"))
+        self._struct = _EmbedStruct(self.n, self.dtype, self.out_dtype, self.tokens, self.width, *self._arrays, self.scale)
+        self.ref = ctypes.byref(self._struct)
+
+
+def _dense(t):
+    """Whether a tensor's elements fill their stretch of memory, in whatever order of dimensions."""
+    if t.is_contiguous() or t.numel() == 0:
+        return True
+    step = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz > 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+class GradList:
+    """Gradient buffers of any types, sizes and dense layouts, taken together;
+    the list keeps references to its tensors.  Built once and reusable across calls."""
+
+    def __init__(self, tensors):
+        self._tensors = list(tensors)
+        self.host, self.count, self._layouts = [], len(self._tensors), []
+        for t in self._tensors:
+            if not _dense(t):
+                raise ValueError("gradients must fill their memory; got strides %s" % (tuple(t.stride()),))
+            self._layouts.append((t.dtype, tuple(t.shape), tuple(t.stride())))
+            _reachable(t, "gradients", self.host)
+        m = max(1, self.count)
+        self.sizes = [t.numel() for t in self._tensors]
+        self._bufs = (ctypes.c_void_p * m)(*[t.data_ptr() or None for t in self._tensors])
+        self._sizes = (ctypes.c_longlong * m)(*self.sizes)
+        self._dtypes = (ctypes.c_int * m)(*[_dtype_code(t.dtype) for t in self._tensors])
+        self._struct = _GradsStruct(self.count, ctypes.cast(self._bufs, ctypes.c_void_p), self._sizes, self._dtypes)
+        self.ref = ctypes.byref(self._struct)
+
+    def like(self, other):
+        """Whether ``other`` has the same types, shapes and strides, buffer by buffer."""
+        return other is self or self._layouts == other._layouts
+
+
+def _reachable(t, what, host):
+    """Notes a tensor in host memory by name (as ``_on_host``) and refuses one on another device than the current one."""
+    if t.is_cuda:
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError("%s must be on the current device, not on device %d" % (what, t.get_device()))
+    elif _on_host(t):
+        host.append(what)
+
+
+def _packed(t, dtypes, numel, what, host):
+    """Address of a contiguous tensor argument of one of ``dtypes`` (integer addresses and None pass through)."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) not in dtypes or t.numel() < numel or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of %s with at least %d elements"
+                         % (what, " or ".join(dtypes), numel))
+    _reachable(t, what, host)
+    return t.data_ptr() or None
+
+
+def _rank_rows(bufs, key, dtype, rows, width, pitches, what, host):
+    """Pointer table of rank buffers; tensors must have the type and hold ``rows[r]`` rows at ``pitches[r]``."""
+    if not isinstance(bufs, PointerTable):
+        bufs = PointerTable(bufs)
+    if bufs._checked != key:
+        if bufs.n != len(rows):
+            raise ValueError("%d rank buffers for %d ranks" % (bufs.n, len(rows)))
+        at = len(host)
+        for b, r, p in zip(bufs._bufs, rows, pitches):
+            if b is None or isinstance(b, int) or r == 0:
+                continue
+            _rows_at(b, dtype, r, width, p, what, host)
+        if len(host) == at:
+            bufs._checked = key
+    return bufs.array
+
+
+def _rows_at(b, dtype, rows, width, pitch, what, host):
+    if str(b.dtype) != _TYPES.get(dtype):
+        raise ValueError("%s of %s do not have the shape's dtype" % (what, b.dtype))
+    room = b.untyped_storage().nbytes() // b.element_size() - b.storage_offset()
+    if room < (rows - 1) * pitch + width:
+        raise ValueError("%s: a buffer of %d elements; %d rows of %d at pitch %d need more" % (what, room, rows, width, pitch))
+    if not _at_pitch(b, pitch, rows):
+        raise ValueError("%s have strides %s; their pitch is %d" % (what, tuple(b.stride()), pitch))
+    _reachable(b, what, host)
+
+
+def _space(w, host):
+    if w is None:
+        return None, 0
+    if not w.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _reachable(w, "workspace", host)
+    return w.data_ptr() or None, w.numel() * w.element_size()
+
+
+def _refuse_host(host, anything=True):
+    if host and anything:
+        raise ValueError("%s must be on the GPU, not in host memory" % host[0])
+
+
+def ar_reduce_norm(partials, shape, weight, out=None, residual=None, summed=None, rstd=None, out8=None, scales=None,
+                   stream=None):
+    """Sum of the n rank buffers and the residual (``summed``), and its RMS norm
+    (``out``; ``out8`` with ``scales``: e4m3 values, a scale to each row or
+    group of columns).  ``rstd`` is what ``ar_reduce_norm_backward`` needs
+    beside ``summed``."""
+    host, r, w = [], shape.rows, shape.width
+    dt = (_TYPES.get(shape.dtype),)
+    args = (_rank_rows(partials, (shape, "partials"), shape.dtype, [r] * shape.n, w, shape.pitches, "partials", host), shape.ref,
+            _packed(weight, (_TYPES.get(shape.weight_dtype),), w, "weight", host),
+            _packed(residual, dt, r * w, "residual", host), _packed(summed, dt, r * w, "summed", host),
+            _packed(out, dt, r * w, "out", host), _packed(rstd, ("torch.float32",), r, "rstd", host),
+            _packed(out8, _BYTES, r * w, "out8", host),
+            _packed(scales, ("torch.float32",), r * shape.groups, "scales", host))
+    _refuse_host(host, r)
+    _check(_lib.ar_reduce_norm(*args, _stream(stream)))
+
+
+def ar_norm_workspace(shape) -> int:
+    """Workspace bytes of ``ar_reduce_norm_backward`` with a weight gradient (host only)."""
+    n = ctypes.c_size_t()
+    _check(_lib.ar_norm_workspace(shape.ref, ctypes.byref(n)))
+    return n.value
+
+
+def ar_reduce_norm_backward(x, shape, weight, rstd, grad_out, grad_x, grad_summed=None, grad_weight=None, workspace=None,
+                            stream=None):
+    """Gradient of the residual and of every partial (``grad_x``), and of the
+    weight, from that of ``out`` and, optionally, of ``summed``.  ``x`` is
+    ``summed`` (its rows may be apart), ``rstd`` from ``ar_reduce_norm``."""
+    host, r, w = [], shape.rows, shape.width
+    dt, f32 = (_TYPES.get(shape.dtype),), ("torch.float32",)
+    pitch = 0
+    if x is not None and not isinstance(x, int):
+        pitch = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else w
+        if r:
+            _rows_at(x, shape.dtype, r, w, pitch, "x", host)
+        x = x.data_ptr() or None
+    ws, wb = _space(workspace, host)
+    args = (x, pitch, shape.ref, _packed(weight, (_TYPES.get(shape.weight_dtype),), w, "weight", host),
+            _packed(rstd, f32, r, "rstd", host), _packed(grad_out, dt, r * w, "grad_out", host),
+            _packed(grad_summed, dt, r * w, "grad_summed", host), _packed(grad_x, dt, r * w, "grad_x", host),
+            _packed(grad_weight, f32, w, "grad_weight", host))
+    _refuse_host(host)
+    _check(_lib.ar_reduce_norm_backward(*args, ws, wb, _stream(stream)))
+
+
+def ar_embedding(tables, shape, token_ids, out, stream=None):
+    """The tokens' rows of a table split by vocabulary entries over the n rank
+    buffers, times the scale; zeros for a token outside the vocabulary."""
+    host, t = [], shape.tokens
+    args = (_rank_rows(tables, (shape, "tables"), shape.dtype, shape.entries, shape.width, shape.pitches, "tables", host),
+            shape.ref, _packed(token_ids, ("torch.int64",), t, "token_ids", host),
+            _packed(out, (_TYPES.get(shape.out_dtype),), t * shape.width, "out", host))
+    _refuse_host(host, t)
+    _check(_lib.ar_embedding(*args, _stream(stream)))
+
+
+def ar_embedding_workspace(shape) -> int:
+    """Workspace bytes of ``ar_embedding_backward`` (host only)."""
+    n = ctypes.c_size_t()
+    _check(_lib.ar_embedding_workspace(shape.ref, ctypes.byref(n)))
+    return n.value
+
+
+def ar_embedding_backward(grad_out, shape, token_ids, grads, accumulate=False, workspace=None, stream=None):
+    """Gradient of every rank's part of the table, zeros in the rows of entries
+    without a token; or, with ``accumulate``, added to what the buffers hold."""
+    host, t = [], shape.tokens
+    ws, wb = _space(workspace, host)
+    table = _rank_rows(grads, (shape, "grads"), shape.dtype, shape.entries, shape.width, shape.grad_pitches, "grads", host)
+    args = (_packed(grad_out, (_TYPES.get(shape.out_dtype),), t * shape.width, "grad_out", host), shape.ref,
+            _packed(token_ids, ("torch.int64",), t, "token_ids", host), table, int(bool(accumulate)))
+    _refuse_host(host, t or not accumulate)
+    _check(_lib.ar_embedding_backward(*args, ws, wb, _stream(stream)))
+
+
+def ar_grad_workspace(grads) -> int:
+    """Workspace bytes of the two calls below (host only)."""
+    n = ctypes.c_size_t()
+    _check(_lib.ar_grad_workspace(grads.ref, ctypes.byref(n)))
+    return n.value
+
+
+def ar_grad_norm(grads, norm, scale=1.0, workspace=None, stream=None):
+    """``scale`` times the 2-norm of all buffers of a ``GradList`` taken together."""
+    host = list(grads.host)
+    ws, wb = _space(workspace, host)
+    norm = _packed(norm, ("torch.float32",), 1, "norm", host)
+    _refuse_host(host)
+    _check(_lib.ar_grad_norm(grads.ref, scale, norm, ws, wb, _stream(stream)))
+
+
+def ar_clip_grads(grads, outs, norm, max_norm, scale=1.0, eps=1e-6, workspace=None, stream=None):
+    """``ar_grad_norm``, and every buffer times ``scale`` and, where the norm is
+    above it, ``max_norm / (norm + eps)``, into the buffers of ``outs`` (in place
+    when ``outs`` is ``grads``)."""
+    if not grads.like(outs):
+        raise ValueError("outs must have the types, shapes and strides of grads")
+    host = grads.host + outs.host
+    ws, wb = _space(workspace, host)
+    norm = _packed(norm, ("torch.float32",), 1, "norm", host)
+    _refuse_host(host)
+    _check(_lib.ar_clip_grads(grads.ref, outs._bufs, max_norm, scale, eps, norm, ws, wb, _stream(stream)))

@@ -1,0 +1,521 @@
+// embed.hip -- embedding lookup from a table split by vocabulary entries over
+// n rank buffers, and its gradient.
+//
+//   out[t] = scale table[token_t],   grad[v] = scale sum_{t : token_t = v} g[t]
+//
+// The lookup reads the ranks' rows where they are: the sum over ranks of rows
+// that all but one leave zero needs no adding.  The gradient sorts the tokens,
+// so that equal ones stand together and no sum needs atomics: the sorted
+// positions are cut into pieces of fixed length, a workgroup adds up the runs
+// of equal tokens in one piece, and the few runs that cross a piece's end are
+// joined by a second launch.  Entries without a token are written as zeros by
+// further workgroups of the same launch.  All of it is bounded by HBM bytes.
+#include "dispatch.hpp"
+#include "layer_device.hpp"
+
+namespace ar {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// ---- ranks -------------------------------------------------------------------
+// The rank that holds entry v of [0, V), found by halving; the same for all lanes.
+template <int NR> __device__ __forceinline__ int rank_of(const EmbedTable<NR> &e, int v) {
+    int lo = 0, hi = e.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (e.first[mid] <= v) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+template <int DT, int NR> __device__ __forceinline__ char *entry_row(const EmbedTable<NR> &e, int v) {
+    const int r = rank_of(e, v);
+    return e.t[r] + (long long)(v - e.first[r]) * e.pitch[r] * elem_bytes<DT>();
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int DT, bool TINY, bool STREAM = true>
+__device__ __forceinline__ void read_row(const char *row, const ColPlace &p, float *v) {
+    widen<DT>(load_at<DT, TINY, STREAM>(row, p), v);
+    settle<TINY>(v, p);
+}
+
+// ---- lookup ------------------------------------------------------------------
+// A wave writes U octs per lane of one token's row.
+template <int DT, int OT, int U, bool TINY, int NR>
+__global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedTable<NR> e, const int64_t *ids, char *out, long long tokens,
+                                                         int width, int slices, int vocab, float scale) {
+    const int lane = threadIdx.x & 63;
+    for (long long item = (long long)blockIdx.x * kWaves + (threadIdx.x >> 6);; item += (long long)gridDim.x * kWaves) {
+        const long long token = item / slices;
+        if (token >= tokens) return;
+        const int oct0 = uniform((int)(item - token * slices)) * 64 * U;
+        const int64_t id = ids[token];
+        const bool known = id >= 0 && id < vocab;
+        const char *row = entry_row<DT>(e, uniform(known ? (int)id : 0));
+        ColPlace p[U];
+        Oct<DT> o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u] = col_place<TINY>(oct0 + u * 64 + lane, width);
+            if (known) o[u] = load_at<DT, TINY, false>(row, p[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[8];
+            if (known) {
+                widen<DT>(o[u], f);
+                settle<TINY>(f, p[u]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = known ? f[i] * scale : 0.0f;
+            store_oct<OT>(out + (token * width + p[u].col) * elem_bytes<OT>(), narrow<OT>(f), p[u].left);
+        }
+    }
+}
+
+// ---- sorting -------------------------------------------------------------------
+__device__ __forceinline__ uint32_t key_of(int64_t id, int vocab) {
+    return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
+}
+
+// Few tokens: a token's place is the number of those before it in the order,
+// (key, position) being compared, counted directly.  A wave counts for eight
+// tokens at once against 64 tokens a step.
+constexpr int kRankEach = 8;
+__global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids, int tokens, int vocab, uint32_t *keys,
+                                                              uint32_t *order) {
+    const int lane = threadIdx.x & 63;
+    const int t0 = uniform((blockIdx.x * kWaves + (threadIdx.x >> 6)) * kRankEach);
+    if (t0 >= tokens) return;
+    uint32_t mine[kRankEach];
+    int before[kRankEach];
+#pragma unroll
+    for (int k = 0; k < kRankEach; ++k) {
+        mine[k] = t0 + k < tokens ? key_of(ids[t0 + k], vocab) : 0u;
+        before[k] = 0;
+    }
+    for (int j0 = 0; j0 < tokens; j0 += 64) {
+        const int j = j0 + lane;
+        // past the end: after everything
+        const uint32_t other = j < tokens ? key_of(ids[j], vocab) : ~0u;
+#pragma unroll
+        for (int k = 0; k < kRankEach; ++k) before[k] += (other < mine[k] || (other == mine[k] && j < t0 + k)) ? 1 : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kRankEach; ++k) {
+        each_bit([&](auto m) { before[k] += (int)lane_xor<m.value>((uint32_t)before[k], lane); });
+        if (t0 + k < tokens && lane == 0) {
+            keys[before[k]] = mine[k];
+            order[before[k]] = (uint32_t)(t0 + k);
+        }
+    }
+}
+
+// Many tokens: stable counting passes over `bits` bits of the key, least
+// significant first.  FIRST reads the ids, others keys and positions.
+struct CountArgs {
+    const int64_t *ids;
+    const uint32_t *keys, *order;
+    uint32_t *keys_to, *order_to;
+    uint32_t *hist;                    // [bins, tiles]
+    uint32_t *totals;                  // [bins]
+    long long tokens, tiles;
+    int vocab, shift, bits, tile;
+};
+template <bool FIRST> __device__ __forceinline__ uint32_t count_key(const CountArgs &a, long long i) {
+    return FIRST ? key_of(a.ids[i], a.vocab) : a.keys[i];
+}
+
+constexpr int kMostBins = 2048;
+
+template <bool FIRST> __global__ __launch_bounds__(kThreads) void embed_count_kernel(const CountArgs a) {
+    __shared__ uint32_t bin[kMostBins];
+    const int bins = 1 << a.bits;
+    for (int b = threadIdx.x; b < bins; b += kThreads) bin[b] = 0;
+    __syncthreads();
+    const long long lo = (long long)blockIdx.x * a.tile, hi = lo + a.tile < a.tokens ? lo + a.tile : a.tokens;
+    for (long long i = lo + threadIdx.x; i < hi; i += kThreads) atomicAdd(&bin[(count_key<FIRST>(a, i) >> a.shift) & (bins - 1)], 1u);
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kThreads) a.hist[b * a.tiles + blockIdx.x] = bin[b];
+}
+
+// Inclusive sum over a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// One workgroup to a bin: how many of the bin's tokens stand in earlier tiles, and in all.
+__global__ __launch_bounds__(kThreads) void embed_tiles_kernel(uint32_t *hist, uint32_t *totals, long long tiles) {
+    __shared__ uint32_t sums[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t *h = hist + (long long)blockIdx.x * tiles;
+    uint32_t base = 0;
+    for (long long t0 = 0; t0 < tiles; t0 += kThreads) {
+        const long long t = t0 + threadIdx.x;
+        const uint32_t v = t < tiles ? h[t] : 0u, in = wave_scan(v, lane);
+        if (lane == 63) sums[wave] = in;
+        __syncthreads();
+        uint32_t before = base;
+        for (int w = 0; w < kWaves; ++w) {
+            before += w < wave ? sums[w] : 0u;
+            base += sums[w];
+        }
+        if (t < tiles) h[t] = before + in - v;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) totals[blockIdx.x] = base;
+}
+
+// Moves a tile's tokens to their places, equal digits in the order they stand in:
+// every wave owns consecutive tokens and counts its own digits first.
+template <bool FIRST> __global__ __launch_bounds__(kThreads) void embed_move_kernel(const CountArgs a) {
+    __shared__ uint32_t place[kWaves][kMostBins];      // next place of a digit's token in each wave
+    __shared__ uint32_t sums[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bins = 1 << a.bits;
+    for (int b = threadIdx.x; b < bins * kWaves; b += kThreads) place[b / bins][b % bins] = 0;
+    __syncthreads();
+    const int each = a.tile / kWaves;                  // a multiple of 64
+    const long long lo = (long long)blockIdx.x * a.tile + (long long)wave * each;
+    const long long hi = lo + each < a.tokens ? lo + each : a.tokens;
+    for (long long i = lo + lane; i < hi; i += 64) atomicAdd(&place[wave][(count_key<FIRST>(a, i) >> a.shift) & (bins - 1)], 1u);
+    __syncthreads();
+    // starts: all lower digits' tokens, this digit's in earlier tiles, in earlier waves
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < bins; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const uint32_t v = b < bins ? a.totals[b] : 0u, in = wave_scan(v, lane);
+        if (lane == 63) sums[wave] = in;
+        __syncthreads();
+        uint32_t start = base + in - v;
+        for (int w = 0; w < kWaves; ++w) {
+            start += w < wave ? sums[w] : 0u;
+            base += sums[w];
+        }
+        if (b < bins) {
+            start += a.hist[b * a.tiles + blockIdx.x];
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t c = place[w][b];
+                place[w][b] = start;
+                start += c;
+            }
+        }
+        __syncthreads();
+    }
+    for (long long i0 = lo; i0 < hi; i0 += 64) {
+        const long long i = i0 + lane;
+        const bool on = i < hi;
+        const uint32_t key = on ? count_key<FIRST>(a, i) : 0u;
+        const uint32_t digit = (key >> a.shift) & (bins - 1);
+        unsigned long long same = __ballot(on);
+        for (int k = 0; k < a.bits; ++k) {
+            const unsigned long long set = __ballot((digit >> k) & 1u);
+            same &= (digit >> k) & 1u ? set : ~set;
+        }
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        uint32_t to = 0;
+        if (on) to = place[wave][digit] + before;
+        __builtin_amdgcn_wave_barrier();
+        if (on && before == 0) place[wave][digit] += __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (on) {
+            a.keys_to[to] = key;
+            a.order_to[to] = FIRST ? (uint32_t)i : a.order[i];
+        }
+    }
+}
+
+// ---- sums ----------------------------------------------------------------------
+struct SumArgs {
+    const uint32_t *keys, *order;
+    const char *g;                     // gradient of the looked-up rows
+    float *part;                       // [pieces, 2, width]: of the run that came in, of the run that goes on
+    long long tokens, pieces;
+    int piece, width, vocab, slices;   // slices of 64 octs of a row
+    int groups;                        // workgroups along a row, a wave to a slice
+    long long sums;                    // workgroups that add; those behind them write zeros
+    float scale;
+    bool accumulate;
+};
+
+template <int DT> __device__ __forceinline__ void write_entry(char *row, const ColPlace &p, const float *v, const SumArgs &a) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[i] * a.scale;
+    char *to = row + (long long)p.col * elem_bytes<DT>();
+    if (a.accumulate) {
+        float old[8];
+        if (p.left >= 8) widen<DT>(load_oct<DT, false>(to), old);
+        else widen<DT>(load_short<DT>(to, p.left), old);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += old[i];
+    }
+    store_oct<DT>(to, narrow<DT>(f), p.left);
+}
+
+// Zeros in the rows of entries [v0, v0 + kZeroRows) that have no token.
+constexpr int kZeroRows = 32;
+template <int DT, int NR> __device__ void zero_rows(const EmbedTable<NR> &e, const SumArgs &a, int v0) {
+    __shared__ uint8_t has[kZeroRows];
+    if (threadIdx.x < kZeroRows) {
+        // the first of the sorted tokens that is not below this entry
+        const uint32_t v = (uint32_t)(v0 + threadIdx.x);
+        long long lo = 0, hi = a.tokens;
+        while (lo < hi) {
+            const long long mid = (lo + hi) / 2;
+            if (a.keys[mid] < v) lo = mid + 1;
+            else hi = mid;
+        }
+        has[threadIdx.x] = lo < a.tokens && a.keys[lo] == v;
+    }
+    __syncthreads();
+    Oct<DT> zero;
+#pragma unroll
+    for (int i = 0; i < (DT == F32 ? 2 : 1); ++i) zero.w[i] = u32x4{0, 0, 0, 0};
+    for (int k = 0; k < kZeroRows && v0 + k < a.vocab; ++k) {
+        if (has[k]) continue;
+        char *row = entry_row<DT>(e, uniform(v0 + k));
+        for (int col = threadIdx.x * 8; col < a.width; col += kThreads * 8)
+            store_oct<DT>(row + (long long)col * elem_bytes<DT>(), zero, a.width - col);
+    }
+}
+
+template <int DT, int OT, bool TINY, int NR>
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(const EmbedTable<NR> e, const SumArgs a) {
+    if (blockIdx.x >= a.sums) {
+        zero_rows<DT>(e, a, (int)(blockIdx.x - a.sums) * kZeroRows);
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    const long long piece = blockIdx.x / a.groups;
+    const int slice = uniform((int)(blockIdx.x - piece * a.groups) * kWaves + (threadIdx.x >> 6));
+    if (slice >= a.slices) return;
+    const ColPlace p = col_place<TINY>(slice * 64 + lane, a.width);
+    const long long s0 = piece * a.piece, s1 = s0 + a.piece < a.tokens ? s0 + a.piece : a.tokens;
+    const uint32_t none = (uint32_t)a.vocab;
+    const uint32_t came = s0 > 0 ? uniform(a.keys[s0 - 1]) : none, goes = s1 < a.tokens ? uniform(a.keys[s1]) : none;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    bool inside = false;               // the run began in this piece
+    uint32_t run = none;
+    constexpr int B = 8;               // rows in flight
+    for (long long s = s0; s < s1; s += B) {
+        uint32_t key[B];
+        Oct<OT> o[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const long long at = s + b < s1 ? s + b : s1 - 1;
+            key[b] = s + b < s1 ? uniform(a.keys[at]) : none;
+            o[b] = load_at<OT, TINY>(a.g + (long long)uniform(a.order[at]) * a.width * elem_bytes<OT>(), p);
+        }
+        if (s == s0) run = key[0], inside = run != came;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (key[b] != run) {
+                if (run != none) {
+                    if (inside) write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
+                    else store_oct<F32, false>((char *)(a.part + (2 * piece) * a.width + p.col), narrow<F32>(sum), p.left);
+                }
+                run = key[b];
+                inside = true;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+            }
+            float v[8];
+            widen<OT>(o[b], v);
+            settle<TINY>(v, p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+        }
+    }
+    if (run == none) return;
+    if (!inside || goes == run)
+        store_oct<F32, false>((char *)(a.part + (2 * piece + (inside ? 1 : 0)) * a.width + p.col), narrow<F32>(sum), p.left);
+    else write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
+}
+
+// The runs that go on past the end of the piece they began in: the waves of a
+// workgroup add up every fourth piece of the run, for 64 octs of the row.
+template <int DT, int NR> __global__ __launch_bounds__(kThreads) void embed_join_kernel(const EmbedTable<NR> e, const SumArgs a) {
+    __shared__ float lds[kWaves][64 * 8];
+    const long long piece = blockIdx.x / a.slices;
+    const int slice = (int)(blockIdx.x - piece * a.slices);
+    const long long s0 = piece * a.piece, s1 = s0 + a.piece;
+    if (s1 >= a.tokens) return;
+    const uint32_t run = uniform(a.keys[s1 - 1]);
+    if (run == (uint32_t)a.vocab || (uint32_t)uniform(a.keys[s1]) != run) return;
+    if (s0 > 0 && (uint32_t)uniform(a.keys[s0 - 1]) == run) return;      // began earlier
+    // the last piece that the run reaches
+    long long lo = piece + 1, hi = a.pieces - 1;
+    while (lo < hi) {
+        const long long mid = (lo + hi + 1) / 2;
+        if ((uint32_t)uniform(a.keys[mid * a.piece]) == run) lo = mid;
+        else hi = mid - 1;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    ColPlace p;
+    p.col = p.at = (slice * 64 + lane) * 8;
+    p.left = a.width - p.col;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    if (p.left > 0) {
+        for (long long q = piece + wave; q <= lo; q += kWaves) {
+            const float *from = a.part + (2 * q + (q == piece ? 1 : 0)) * a.width + p.col;
+            float v[8];
+            if (p.left >= 8) widen<F32>(load_oct<F32, false>((const char *)from), v);
+            else widen<F32>(load_short<F32>((const char *)from, p.left), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lds[wave][i * 64 + lane] = sum[i];
+    __syncthreads();
+    if (wave == 0 && p.left > 0) {
+        for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += lds[w][i * 64 + lane];
+        write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
+    }
+}
+
+// ---- host ----------------------------------------------------------------------
+template <int NR> EmbedTable<NR> table_of(const EmbedCall &c) {
+    EmbedTable<NR> e;
+    int first = 0;
+    for (int r = 0; r < NR; ++r) {
+        e.t[r] = r < c.n ? (char *)c.t[r] : nullptr;
+        e.pitch[r] = r < c.n ? (uint32_t)c.pitches[r] : 0;
+        e.first[r] = first;
+        if (r < c.n) first += (int)c.entries[r];
+    }
+    e.first[NR] = first;
+    e.n = c.n;
+    return e;
+}
+
+template <typename F> hipError_t by_type(int dtype, F &&f) {
+    switch (dtype) {
+    case F32: return f(std::integral_constant<int, F32>{});
+    case BF16: return f(std::integral_constant<int, BF16>{});
+    case F16: return f(std::integral_constant<int, F16>{});
+    default: return hipErrorInvalidValue;
+    }
+}
+// f(table's type, rows' type, ranks of the pointer table, whether rows are shorter than an oct)
+template <typename F> hipError_t dispatch_embed(const EmbedCall &c, F &&f) {
+    return by_type(c.dtype, [&](auto dt) {
+        return by_type(c.out_dtype, [&](auto ot) {
+            constexpr std::integral_constant<int, kLayerFew> few{};
+            constexpr std::integral_constant<int, kLayerMany> many{};
+            if (c.width < 8) return f(dt, ot, many, std::true_type{});
+            return c.n <= kLayerFew ? f(dt, ot, few, std::false_type{}) : f(dt, ot, many, std::false_type{});
+        });
+    });
+}
+
+constexpr long long kMostGroups = 1 << 22;             // a grid's threads stay below 2^32
+int octs_of(int width) { return (width + 7) / 8; }
+
+}  // namespace
+
+hipError_t launch_embedding(const EmbedCall &c, void *out, hipStream_t s) {
+    constexpr int U = 2;
+    const int slices = (octs_of(c.width) + 64 * U - 1) / (64 * U);
+    const long long all = (c.tokens * slices + kWaves - 1) / kWaves, groups = all < kMostGroups ? all : kMostGroups;
+    return dispatch_embed(c, [&](auto dt, auto ot, auto nr, auto tiny) {
+        return launch(embed_kernel<dt.value, ot.value, U, tiny.value, nr.value>, dim3((unsigned)groups), dim3(kThreads), 0, s,
+                      table_of<nr.value>(c), c.ids, (char *)out, c.tokens, c.width, slices, c.vocab, c.scale);
+    });
+}
+
+EmbedSpace embed_space(long long tokens, int width, int vocab) {
+    EmbedSpace w{};
+    const auto add = [&](size_t bytes) {
+        const size_t at = w.bytes;
+        w.bytes += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    w.piece = 16;
+    while (w.piece < 4096 && w.piece * 1024LL < tokens) w.piece *= 2;
+    w.pieces = (tokens + w.piece - 1) / w.piece;
+    w.keys = add(tokens * 4);
+    w.order = add(tokens * 4);
+    if (tokens > 8192) {
+        int bits = 1;
+        while ((1 << bits) <= vocab) ++bits;            // the key `vocab` among them
+        w.passes = bits <= 11 ? 1 : 2;
+        w.digit = (bits + w.passes - 1) / w.passes;
+        w.tile = 1024;
+        while (w.tile * 1024LL < tokens) w.tile *= 2;
+        w.tiles = (tokens + w.tile - 1) / w.tile;
+        w.keys2 = add(tokens * 4);
+        w.order2 = add(tokens * 4);
+        w.hist = add(((size_t)w.tiles << w.digit) * 4);
+        w.totals = add((size_t)4 << w.digit);
+    }
+    w.part = add((size_t)w.pieces * 2 * width * 4);
+    return w;
+}
+
+hipError_t launch_embed_sort(const EmbedCall &c, const EmbedSpace &w, char *space, hipStream_t s) {
+    uint32_t *keys = (uint32_t *)(space + w.keys), *order = (uint32_t *)(space + w.order);
+    if (w.passes == 0) {
+        const unsigned groups = (unsigned)((c.tokens + kWaves * kRankEach - 1) / (kWaves * kRankEach));
+        return launch(embed_rank_kernel, dim3(groups), dim3(kThreads), 0, s, c.ids, (int)c.tokens, c.vocab, keys, order);
+    }
+    uint32_t *keys2 = (uint32_t *)(space + w.keys2), *order2 = (uint32_t *)(space + w.order2);
+    hipError_t e = hipSuccess;
+    for (int pass = 0; pass < w.passes && e == hipSuccess; ++pass) {
+        const bool last = pass == w.passes - 1;
+        CountArgs a{c.ids, keys2, order2, last ? keys : keys2, last ? order : order2, (uint32_t *)(space + w.hist),
+                    (uint32_t *)(space + w.totals), c.tokens, w.tiles, c.vocab, pass * w.digit, w.digit, w.tile};
+        const dim3 grid((unsigned)w.tiles), block(kThreads);
+        e = launch(pass ? embed_count_kernel<false> : embed_count_kernel<true>, grid, block, 0, s, a);
+        if (e == hipSuccess) e = launch(embed_tiles_kernel, dim3(1u << w.digit), block, 0, s, a.hist, a.totals, w.tiles);
+        if (e == hipSuccess) e = launch(pass ? embed_move_kernel<false> : embed_move_kernel<true>, grid, block, 0, s, a);
+    }
+    return e;
+}
+
+hipError_t launch_embed_sum(const EmbedCall &c, const EmbedSpace &w, char *space, const void *grad_out, hipStream_t s) {
+    SumArgs a{};
+    a.keys = (const uint32_t *)(space + w.keys);
+    a.order = (const uint32_t *)(space + w.order);
+    a.g = (const char *)grad_out;
+    a.part = (float *)(space + w.part);
+    a.tokens = c.tokens;
+    a.pieces = w.pieces;
+    a.piece = w.piece;
+    a.width = c.width;
+    a.vocab = c.vocab;
+    a.slices = (octs_of(c.width) + 63) / 64;
+    a.groups = (a.slices + kWaves - 1) / kWaves;
+    a.sums = w.pieces * a.groups;
+    a.scale = c.scale;
+    a.accumulate = c.accumulate;
+    const long long zeros = c.accumulate ? 0 : (c.vocab + kZeroRows - 1) / kZeroRows;
+    return dispatch_embed(c, [&](auto dt, auto ot, auto nr, auto tiny) {
+        const EmbedTable<nr.value> e = table_of<nr.value>(c);
+        hipError_t st = hipSuccess;
+        if (a.sums + zeros)
+            st = launch(embed_sum_kernel<dt.value, ot.value, tiny.value, nr.value>, dim3((unsigned)(a.sums + zeros)),
+                        dim3(kThreads), 0, s, e, a);
+        if (st == hipSuccess && w.pieces > 1)
+            st = launch(embed_join_kernel<dt.value, nr.value>, dim3((unsigned)((w.pieces - 1) * a.slices)), dim3(kThreads), 0, s,
+                        e, a);
+        return st;
+    });
+}
+
+}  // namespace ar
