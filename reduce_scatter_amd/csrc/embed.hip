@@ -37,42 +37,41 @@ template <int DT, int NR> __device__ __forceinline__ char *entry_row(const Embed
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int DT, bool TINY, bool STREAM = true>
-__device__ __forceinline__ void read_row(const char *row, const ColPlace &p, float *v) {
-    widen<DT>(load_at<DT, TINY, STREAM>(row, p), v);
-    settle<TINY>(v, p);
-}
+// Columns to a lane: 16 bytes of the wider type.
+template <int DT, int OT> constexpr int kCols = DT == F32 || OT == F32 ? 4 : 8;
 
 // ---- lookup ------------------------------------------------------------------
-// A wave writes U octs per lane of one token's row.
-template <int DT, int OT, int U, bool TINY, int NR>
+// A wave writes U runs per lane of one token's row.
+constexpr int kLookupCols = 1024;      // of a wave
+template <int DT, int OT, bool TINY, int NR>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedTable<NR> e, const int64_t *ids, char *out, long long tokens,
                                                          int width, int slices, int vocab, float scale) {
+    constexpr int K = kCols<DT, OT>, U = kLookupCols / 64 / K;
     const int lane = threadIdx.x & 63;
     for (long long item = (long long)blockIdx.x * kWaves + (threadIdx.x >> 6);; item += (long long)gridDim.x * kWaves) {
         const long long token = item / slices;
         if (token >= tokens) return;
-        const int oct0 = uniform((int)(item - token * slices)) * 64 * U;
+        const int run0 = uniform((int)(item - token * slices)) * 64 * U;
         const int64_t id = ids[token];
         const bool known = id >= 0 && id < vocab;
         const char *row = entry_row<DT>(e, uniform(known ? (int)id : 0));
         ColPlace p[U];
-        Oct<DT> o[U];
+        Run<DT, K> o[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            p[u] = col_place<TINY>(oct0 + u * 64 + lane, width);
-            if (known) o[u] = load_at<DT, TINY, false>(row, p[u]);
+            p[u] = col_place<K, TINY>(run0 + u * 64 + lane, width);
+            if (known) o[u] = load_at<DT, K, TINY, false>(row, p[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float f[8];
+            float f[K];
             if (known) {
-                widen<DT>(o[u], f);
-                settle<TINY>(f, p[u]);
+                widen<DT, K>(o[u], f);
+                settle<K, TINY>(f, p[u]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = known ? f[i] * scale : 0.0f;
-            store_oct<OT>(out + (token * width + p[u].col) * elem_bytes<OT>(), narrow<OT>(f), p[u].left);
+            for (int i = 0; i < K; ++i) f[i] = known ? f[i] * scale : 0.0f;
+            store_run<OT, K>(out + (token * width + p[u].col) * elem_bytes<OT>(), narrow<OT, K>(f), p[u].left);
         }
     }
 }
@@ -84,10 +83,31 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, int vocab) {
 
 // Few tokens: a token's place is the number of those before it in the order,
 // (key, position) being compared, counted directly.  A wave counts for eight
-// tokens at once against 64 tokens a step.
+// tokens at once against 64 tokens a step.  The workgroups behind those write
+// which entries have a token, kMapEach of them each.
 constexpr int kRankEach = 8;
+constexpr int kMapEach = 1024;
 __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids, int tokens, int vocab, uint32_t *keys,
-                                                              uint32_t *order) {
+                                                              uint32_t *order, uint8_t *map, int ranks) {
+    __shared__ uint32_t has[kMapEach / 4];
+    if ((int)blockIdx.x >= ranks) {
+        const int v0 = ((int)blockIdx.x - ranks) * kMapEach;
+        has[threadIdx.x] = 0;
+        __syncthreads();
+        constexpr int B = 4;
+        for (int i = threadIdx.x; i < tokens; i += B * kThreads) {
+            uint32_t k[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) k[b] = i + b * kThreads < tokens ? key_of(ids[i + b * kThreads], vocab) - (uint32_t)v0 : ~0u;
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                if (k[b] < kMapEach) ((uint8_t *)has)[k[b]] = 1;
+        }
+        __syncthreads();
+        // the map has room for whole workgroups
+        ((uint32_t *)(map + v0))[threadIdx.x] = has[threadIdx.x];
+        return;
+    }
     const int lane = threadIdx.x & 63;
     const int t0 = uniform((blockIdx.x * kWaves + (threadIdx.x >> 6)) * kRankEach);
     if (t0 >= tokens) return;
@@ -98,12 +118,19 @@ __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids
         mine[k] = t0 + k < tokens ? key_of(ids[t0 + k], vocab) : 0u;
         before[k] = 0;
     }
-    for (int j0 = 0; j0 < tokens; j0 += 64) {
-        const int j = j0 + lane;
-        // past the end: after everything
-        const uint32_t other = j < tokens ? key_of(ids[j], vocab) : ~0u;
+    constexpr int B = 4;
+    for (int j0 = 0; j0 < tokens; j0 += 64 * B) {
+        uint32_t other[B];
 #pragma unroll
-        for (int k = 0; k < kRankEach; ++k) before[k] += (other < mine[k] || (other == mine[k] && j < t0 + k)) ? 1 : 0;
+        for (int b = 0; b < B; ++b) {
+            const int j = j0 + b * 64 + lane;
+            other[b] = j < tokens ? key_of(ids[j], vocab) : ~0u;      // past the end: after everything
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int k = 0; k < kRankEach; ++k)
+                before[k] += (other[b] < mine[k] || (other[b] == mine[k] && j0 + b * 64 + lane < t0 + k)) ? 1 : 0;
     }
 #pragma unroll
     for (int k = 0; k < kRankEach; ++k) {
@@ -116,13 +143,15 @@ __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids
 }
 
 // Many tokens: stable counting passes over `bits` bits of the key, least
-// significant first.  FIRST reads the ids, others keys and positions.
+// significant first.  FIRST reads the ids, others keys and positions; it also
+// clears (counting) and sets (moving) the map of entries that have a token.
 struct CountArgs {
     const int64_t *ids;
     const uint32_t *keys, *order;
     uint32_t *keys_to, *order_to;
     uint32_t *hist;                    // [bins, tiles]
     uint32_t *totals;                  // [bins]
+    uint32_t *map;                     // [vocab] bytes, of whole words
     long long tokens, tiles;
     int vocab, shift, bits, tile;
 };
@@ -136,6 +165,9 @@ template <bool FIRST> __global__ __launch_bounds__(kThreads) void embed_count_ke
     __shared__ uint32_t bin[kMostBins];
     const int bins = 1 << a.bits;
     for (int b = threadIdx.x; b < bins; b += kThreads) bin[b] = 0;
+    if (FIRST)
+        for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < (a.vocab + 3) / 4; i += (long long)gridDim.x * kThreads)
+            a.map[i] = 0;
     __syncthreads();
     const long long lo = (long long)blockIdx.x * a.tile, hi = lo + a.tile < a.tokens ? lo + a.tile : a.tokens;
     for (long long i = lo + threadIdx.x; i < hi; i += kThreads) atomicAdd(&bin[(count_key<FIRST>(a, i) >> a.shift) & (bins - 1)], 1u);
@@ -227,6 +259,7 @@ template <bool FIRST> __global__ __launch_bounds__(kThreads) void embed_move_ker
         if (on && before == 0) place[wave][digit] += __popcll(same);
         __builtin_amdgcn_wave_barrier();
         if (on) {
+            if (FIRST && key < (uint32_t)a.vocab) ((uint8_t *)a.map)[key] = 1;     // every writer writes the same
             a.keys_to[to] = key;
             a.order_to[to] = FIRST ? (uint32_t)i : a.order[i];
         }
@@ -237,156 +270,173 @@ template <bool FIRST> __global__ __launch_bounds__(kThreads) void embed_move_ker
 struct SumArgs {
     const uint32_t *keys, *order;
     const char *g;                     // gradient of the looked-up rows
-    float *part;                       // [pieces, 2, width]: of the run that came in, of the run that goes on
+    float *part;                       // [pieces, 2, part_width]: of the run that came in, of the run that goes on
     long long tokens, pieces;
-    int piece, width, vocab, slices;   // slices of 64 octs of a row
+    int piece, width, part_width, vocab;
+    int slices;                        // of 64 runs of a row
     int groups;                        // workgroups along a row, a wave to a slice
     long long sums;                    // workgroups that add; those behind them write zeros
+    const uint8_t *map;                // which entries have a token; NULL: none has
+    int zero_rows, zero_lanes;
     float scale;
     bool accumulate;
 };
 
-template <int DT> __device__ __forceinline__ void write_entry(char *row, const ColPlace &p, const float *v, const SumArgs &a) {
-    float f[8];
+template <int DT, int K> __device__ __forceinline__ void write_entry(char *row, const ColPlace &p, const float *v, const SumArgs &a) {
+    float f[K];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = v[i] * a.scale;
+    for (int i = 0; i < K; ++i) f[i] = v[i] * a.scale;
     char *to = row + (long long)p.col * elem_bytes<DT>();
     if (a.accumulate) {
-        float old[8];
-        if (p.left >= 8) widen<DT>(load_oct<DT, false>(to), old);
-        else widen<DT>(load_short<DT>(to, p.left), old);
+        float old[K];
+        if (p.left >= K) widen<DT, K>(load_run<DT, K, false>(to), old);
+        else widen<DT, K>(load_short<DT, K>(to, p.left), old);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += old[i];
+        for (int i = 0; i < K; ++i) f[i] += old[i];
     }
-    store_oct<DT>(to, narrow<DT>(f), p.left);
+    store_run<DT, K>(to, narrow<DT, K>(f), p.left);
 }
 
-// Zeros in the rows of entries [v0, v0 + kZeroRows) that have no token.
-constexpr int kZeroRows = 32;
-template <int DT, int NR> __device__ void zero_rows(const EmbedTable<NR> &e, const SumArgs &a, int v0) {
-    __shared__ uint8_t has[kZeroRows];
-    if (threadIdx.x < kZeroRows) {
-        // the first of the sorted tokens that is not below this entry
-        const uint32_t v = (uint32_t)(v0 + threadIdx.x);
-        long long lo = 0, hi = a.tokens;
-        while (lo < hi) {
-            const long long mid = (lo + hi) / 2;
-            if (a.keys[mid] < v) lo = mid + 1;
-            else hi = mid;
-        }
-        has[threadIdx.x] = lo < a.tokens && a.keys[lo] == v;
-    }
-    __syncthreads();
-    Oct<DT> zero;
+// A slice's partial sums: four columns of every lane after the other.
+template <int K> __device__ __forceinline__ float *part_of(const SumArgs &a, long long piece, int which, int slice, int lane) {
+    return a.part + (2 * piece + which) * a.part_width + slice * 64 * K + lane * 4;
+}
+template <int K> __device__ __forceinline__ void write_part(float *to, const float *v) {
 #pragma unroll
-    for (int i = 0; i < (DT == F32 ? 2 : 1); ++i) zero.w[i] = u32x4{0, 0, 0, 0};
-    for (int k = 0; k < kZeroRows && v0 + k < a.vocab; ++k) {
-        if (has[k]) continue;
-        char *row = entry_row<DT>(e, uniform(v0 + k));
-        for (int col = threadIdx.x * 8; col < a.width; col += kThreads * 8)
-            store_oct<DT>(row + (long long)col * elem_bytes<DT>(), zero, a.width - col);
+    for (int j = 0; j < K / 4; ++j) store_run<F32, 4, false>((char *)(to + j * 256), narrow<F32, 4>(v + 4 * j), 4);
+}
+
+// Zeros in the rows of entries without a token, a.zero_rows of them to a
+// workgroup, a.zero_lanes lanes (a power of two) to a row.
+template <int DT, int NR> __device__ __forceinline__ void zero_rows(const EmbedTable<NR> &e, const SumArgs &a, long long group) {
+    const int sets = kThreads / a.zero_lanes, lane = threadIdx.x & (a.zero_lanes - 1);
+    const int bytes = a.width * elem_bytes<DT>();
+    const long long v0 = group * a.zero_rows, v1 = v0 + a.zero_rows < a.vocab ? v0 + a.zero_rows : a.vocab;
+    for (long long v = v0 + threadIdx.x / a.zero_lanes; v < v1; v += sets) {
+        if (a.map && a.map[v]) continue;
+        char *row = entry_row<DT>(e, a.zero_lanes >= 64 ? uniform((int)v) : (int)v);
+        for (int at = lane * 16; at < bytes; at += a.zero_lanes * 16) {
+            if (bytes - at >= 16) {
+                __builtin_nontemporal_store(u32x4e{0, 0, 0, 0}, (u32x4e *)(row + at));
+            } else {
+                for (int i = at; i < bytes; i += 2) *(uint16_t *)(row + i) = 0;
+            }
+        }
     }
 }
 
 template <int DT, int OT, bool TINY, int NR>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const EmbedTable<NR> e, const SumArgs a) {
+    constexpr int K = kCols<DT, OT>;
     if (blockIdx.x >= a.sums) {
-        zero_rows<DT>(e, a, (int)(blockIdx.x - a.sums) * kZeroRows);
+        zero_rows<DT>(e, a, blockIdx.x - a.sums);
         return;
     }
     const int lane = threadIdx.x & 63;
     const long long piece = blockIdx.x / a.groups;
     const int slice = uniform((int)(blockIdx.x - piece * a.groups) * kWaves + (threadIdx.x >> 6));
     if (slice >= a.slices) return;
-    const ColPlace p = col_place<TINY>(slice * 64 + lane, a.width);
+    const ColPlace p = col_place<K, TINY>(slice * 64 + lane, a.width);
     const long long s0 = piece * a.piece, s1 = s0 + a.piece < a.tokens ? s0 + a.piece : a.tokens;
-    const uint32_t none = (uint32_t)a.vocab;
-    const uint32_t came = s0 > 0 ? uniform(a.keys[s0 - 1]) : none, goes = s1 < a.tokens ? uniform(a.keys[s1]) : none;
-    float sum[8];
+    const int none = a.vocab;
+    const int came = s0 > 0 ? uniform(a.keys[s0 - 1]) : none, goes = s1 < a.tokens ? uniform(a.keys[s1]) : none;
+    float sum[K];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    for (int i = 0; i < K; ++i) sum[i] = 0.0f;
     bool inside = false;               // the run began in this piece
-    uint32_t run = none;
-    constexpr int B = 8;               // rows in flight
-    for (long long s = s0; s < s1; s += B) {
-        uint32_t key[B];
-        Oct<OT> o[B];
+    int run = came;
+    for (long long s = s0; s < s1; s += 64) {
+        // 64 tokens' keys and positions, a lane to each; the rows of eight are in flight at a time
+        const int n = s1 - s < 64 ? (int)(s1 - s) : 64;
+        const long long at = s + (lane < n ? lane : n - 1);
+        const int keys = (int)a.keys[at], order = (int)a.order[at];
+        constexpr int B = 8;
+        for (int b0 = 0; b0 < n; b0 += B) {
+            Run<OT, K> o[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const long long at = s + b < s1 ? s + b : s1 - 1;
-            key[b] = s + b < s1 ? uniform(a.keys[at]) : none;
-            o[b] = load_at<OT, TINY>(a.g + (long long)uniform(a.order[at]) * a.width * elem_bytes<OT>(), p);
-        }
-        if (s == s0) run = key[0], inside = run != came;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            if (key[b] != run) {
-                if (run != none) {
-                    if (inside) write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
-                    else store_oct<F32, false>((char *)(a.part + (2 * piece) * a.width + p.col), narrow<F32>(sum), p.left);
-                }
-                run = key[b];
-                inside = true;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+            for (int b = 0; b < B; ++b) {
+                const long long row = (uint32_t)__builtin_amdgcn_readlane(order, b0 + b);
+                o[b] = load_at<OT, K, TINY>(a.g + row * a.width * elem_bytes<OT>(), p);
             }
-            float v[8];
-            widen<OT>(o[b], v);
-            settle<TINY>(v, p);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+            for (int b = 0; b < B; ++b) {
+                const int key = b0 + b < n ? __builtin_amdgcn_readlane(keys, b0 + b) : none;
+                if (key != run) {
+                    if (run != none) {
+                        if (inside) write_entry<DT, K>(entry_row<DT>(e, run), p, sum, a);
+                        else if (s + b0 + b > s0) write_part<K>(part_of<K>(a, piece, 0, slice, lane), sum);
+                    }
+                    run = key;
+                    inside = true;
+#pragma unroll
+                    for (int i = 0; i < K; ++i) sum[i] = 0.0f;
+                }
+                float v[K];
+                widen<OT, K>(o[b], v);
+                settle<K, TINY>(v, p);
+#pragma unroll
+                for (int i = 0; i < K; ++i) sum[i] += v[i];
+            }
+            if (run == none) return;   // no tokens from here on
         }
     }
-    if (run == none) return;
-    if (!inside || goes == run)
-        store_oct<F32, false>((char *)(a.part + (2 * piece + (inside ? 1 : 0)) * a.width + p.col), narrow<F32>(sum), p.left);
-    else write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
+    if (inside && goes != run) write_entry<DT, K>(entry_row<DT>(e, run), p, sum, a);
+    else write_part<K>(part_of<K>(a, piece, inside ? 1 : 0, slice, lane), sum);
 }
 
 // The runs that go on past the end of the piece they began in: the waves of a
-// workgroup add up every fourth piece of the run, for 64 octs of the row.
-template <int DT, int NR> __global__ __launch_bounds__(kThreads) void embed_join_kernel(const EmbedTable<NR> e, const SumArgs a) {
-    __shared__ float lds[kWaves][64 * 8];
+// workgroup add up every fourth piece of the run, for a slice of the row.
+template <int DT, int K, int NR>
+__global__ __launch_bounds__(kThreads) void embed_join_kernel(const EmbedTable<NR> e, const SumArgs a) {
+    __shared__ float lds[kWaves][64 * K];
     const long long piece = blockIdx.x / a.slices;
     const int slice = (int)(blockIdx.x - piece * a.slices);
     const long long s0 = piece * a.piece, s1 = s0 + a.piece;
     if (s1 >= a.tokens) return;
-    const uint32_t run = uniform(a.keys[s1 - 1]);
-    if (run == (uint32_t)a.vocab || (uint32_t)uniform(a.keys[s1]) != run) return;
-    if (s0 > 0 && (uint32_t)uniform(a.keys[s0 - 1]) == run) return;      // began earlier
-    // the last piece that the run reaches
-    long long lo = piece + 1, hi = a.pieces - 1;
-    while (lo < hi) {
-        const long long mid = (lo + hi + 1) / 2;
-        if ((uint32_t)uniform(a.keys[mid * a.piece]) == run) lo = mid;
-        else hi = mid - 1;
-    }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    ColPlace p;
-    p.col = p.at = (slice * 64 + lane) * 8;
-    p.left = a.width - p.col;
-    float sum[8];
+    const int before = s0 > 0 ? (int)a.keys[s0 - 1] : a.vocab, last = (int)a.keys[s1 - 1], after = (int)a.keys[s1];
+    const int run = uniform(last);
+    if (run == a.vocab || uniform(after) != run || uniform(before) == run) return;      // none, ends here, began earlier
+    // the last piece that the run reaches: pieces that begin with it, 64 looked at a time
+    long long end = piece + 1;
+    for (;;) {
+        const long long q = end + lane;
+        const unsigned long long same = __ballot(q < a.pieces && (int)a.keys[q < a.pieces ? q * a.piece : 0] == run);
+        end += same == ~0ull ? 64 : __builtin_ctzll(~same);
+        if (same != ~0ull) break;
+    }
+    float sum[K];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-    if (p.left > 0) {
-        for (long long q = piece + wave; q <= lo; q += kWaves) {
-            const float *from = a.part + (2 * q + (q == piece ? 1 : 0)) * a.width + p.col;
-            float v[8];
-            if (p.left >= 8) widen<F32>(load_oct<F32, false>((const char *)from), v);
-            else widen<F32>(load_short<F32>((const char *)from, p.left), v);
+    for (int i = 0; i < K; ++i) sum[i] = 0.0f;
+    constexpr int B = 4;
+    for (long long q = piece + wave; q < end; q += B * kWaves) {
+        Run<F32, 4> o[B][K / 4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+        for (int b = 0; b < B; ++b) {
+            const long long at = q + b * kWaves;
+            if (at < end)
+#pragma unroll
+                for (int j = 0; j < K / 4; ++j)
+                    o[b][j] = load_run<F32, 4, false>((const char *)(part_of<K>(a, at, at == piece ? 1 : 0, slice, lane) + j * 256));
         }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (q + b * kWaves < end)
+#pragma unroll
+                for (int i = 0; i < K; ++i) sum[i] += bits_f32(o[b][i / 4].w[i % 4]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lds[wave][i * 64 + lane] = sum[i];
+    for (int i = 0; i < K; ++i) lds[wave][i * 64 + lane] = sum[i];
     __syncthreads();
-    if (wave == 0 && p.left > 0) {
-        for (int w = 1; w < kWaves; ++w)
+    if (wave != 0) return;
+    ColPlace p;
+    p.col = p.at = (slice * 64 + lane) * K;
+    p.left = a.width - p.col;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += lds[w][i * 64 + lane];
-        write_entry<DT>(entry_row<DT>(e, (int)run), p, sum, a);
-    }
+    for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+        for (int i = 0; i < K; ++i) sum[i] += lds[w][i * 64 + lane];
+    if (p.left > 0) write_entry<DT, K>(entry_row<DT>(e, run), p, sum, a);
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -412,7 +462,7 @@ template <typename F> hipError_t by_type(int dtype, F &&f) {
     default: return hipErrorInvalidValue;
     }
 }
-// f(table's type, rows' type, ranks of the pointer table, whether rows are shorter than an oct)
+// f(table's type, rows' type, ranks of the pointer table, whether rows are shorter than eight columns)
 template <typename F> hipError_t dispatch_embed(const EmbedCall &c, F &&f) {
     return by_type(c.dtype, [&](auto dt) {
         return by_type(c.out_dtype, [&](auto ot) {
@@ -425,22 +475,29 @@ template <typename F> hipError_t dispatch_embed(const EmbedCall &c, F &&f) {
 }
 
 constexpr long long kMostGroups = 1 << 22;             // a grid's threads stay below 2^32
-int octs_of(int width) { return (width + 7) / 8; }
+// Slices of 64 runs of a row.
+int slices_of(const EmbedCall &c) {
+    const int cols = 64 * (c.dtype == F32 || c.out_dtype == F32 ? 4 : 8);
+    return (c.width + cols - 1) / cols;
+}
 
 }  // namespace
 
 hipError_t launch_embedding(const EmbedCall &c, void *out, hipStream_t s) {
-    constexpr int U = 2;
-    const int slices = (octs_of(c.width) + 64 * U - 1) / (64 * U);
+    const int slices = (c.width + kLookupCols - 1) / kLookupCols;
     const long long all = (c.tokens * slices + kWaves - 1) / kWaves, groups = all < kMostGroups ? all : kMostGroups;
     return dispatch_embed(c, [&](auto dt, auto ot, auto nr, auto tiny) {
-        return launch(embed_kernel<dt.value, ot.value, U, tiny.value, nr.value>, dim3((unsigned)groups), dim3(kThreads), 0, s,
+        return launch(embed_kernel<dt.value, ot.value, tiny.value, nr.value>, dim3((unsigned)groups), dim3(kThreads), 0, s,
                       table_of<nr.value>(c), c.ids, (char *)out, c.tokens, c.width, slices, c.vocab, c.scale);
     });
 }
 
+// Places of a partial sum: whole slices, of the longer kind.
+static int part_width(int width) { return (width + 511) / 512 * 512; }
+
 EmbedSpace embed_space(long long tokens, int width, int vocab) {
     EmbedSpace w{};
+    if (tokens == 0) return w;
     const auto add = [&](size_t bytes) {
         const size_t at = w.bytes;
         w.bytes += (bytes + 255) / 256 * 256;
@@ -451,12 +508,13 @@ EmbedSpace embed_space(long long tokens, int width, int vocab) {
     w.pieces = (tokens + w.piece - 1) / w.piece;
     w.keys = add(tokens * 4);
     w.order = add(tokens * 4);
+    w.map = add((size_t)(vocab + kMapEach - 1) / kMapEach * kMapEach);
     if (tokens > 8192) {
         int bits = 1;
         while ((1 << bits) <= vocab) ++bits;            // the key `vocab` among them
         w.passes = bits <= 11 ? 1 : 2;
         w.digit = (bits + w.passes - 1) / w.passes;
-        w.tile = 1024;
+        w.tile = 256;
         while (w.tile * 1024LL < tokens) w.tile *= 2;
         w.tiles = (tokens + w.tile - 1) / w.tile;
         w.keys2 = add(tokens * 4);
@@ -464,22 +522,24 @@ EmbedSpace embed_space(long long tokens, int width, int vocab) {
         w.hist = add(((size_t)w.tiles << w.digit) * 4);
         w.totals = add((size_t)4 << w.digit);
     }
-    w.part = add((size_t)w.pieces * 2 * width * 4);
+    w.part = add((size_t)w.pieces * 2 * part_width(width) * 4);
     return w;
 }
 
 hipError_t launch_embed_sort(const EmbedCall &c, const EmbedSpace &w, char *space, hipStream_t s) {
     uint32_t *keys = (uint32_t *)(space + w.keys), *order = (uint32_t *)(space + w.order);
     if (w.passes == 0) {
-        const unsigned groups = (unsigned)((c.tokens + kWaves * kRankEach - 1) / (kWaves * kRankEach));
-        return launch(embed_rank_kernel, dim3(groups), dim3(kThreads), 0, s, c.ids, (int)c.tokens, c.vocab, keys, order);
+        const int ranks = (int)((c.tokens + kWaves * kRankEach - 1) / (kWaves * kRankEach));
+        const int maps = c.accumulate ? 0 : (c.vocab + kMapEach - 1) / kMapEach;
+        return launch(embed_rank_kernel, dim3((unsigned)(ranks + maps)), dim3(kThreads), 0, s, c.ids, (int)c.tokens, c.vocab, keys, order,
+                      (uint8_t *)(space + w.map), ranks);
     }
     uint32_t *keys2 = (uint32_t *)(space + w.keys2), *order2 = (uint32_t *)(space + w.order2);
     hipError_t e = hipSuccess;
     for (int pass = 0; pass < w.passes && e == hipSuccess; ++pass) {
         const bool last = pass == w.passes - 1;
         CountArgs a{c.ids, keys2, order2, last ? keys : keys2, last ? order : order2, (uint32_t *)(space + w.hist),
-                    (uint32_t *)(space + w.totals), c.tokens, w.tiles, c.vocab, pass * w.digit, w.digit, w.tile};
+                    (uint32_t *)(space + w.totals), (uint32_t *)(space + w.map), c.tokens, w.tiles, c.vocab, pass * w.digit, w.digit, w.tile};
         const dim3 grid((unsigned)w.tiles), block(kThreads);
         e = launch(pass ? embed_count_kernel<false> : embed_count_kernel<true>, grid, block, 0, s, a);
         if (e == hipSuccess) e = launch(embed_tiles_kernel, dim3(1u << w.digit), block, 0, s, a.hist, a.totals, w.tiles);
@@ -499,12 +559,21 @@ hipError_t launch_embed_sum(const EmbedCall &c, const EmbedSpace &w, char *space
     a.piece = w.piece;
     a.width = c.width;
     a.vocab = c.vocab;
-    a.slices = (octs_of(c.width) + 63) / 64;
+    a.part_width = part_width(c.width);
+    a.slices = slices_of(c);
     a.groups = (a.slices + kWaves - 1) / kWaves;
     a.sums = w.pieces * a.groups;
     a.scale = c.scale;
     a.accumulate = c.accumulate;
-    const long long zeros = c.accumulate ? 0 : (c.vocab + kZeroRows - 1) / kZeroRows;
+    // About 16 KB to a workgroup, neighbouring rows to neighbouring ones: a fill of 1 GB wrote 6.1 TB/s with 8 KB to a
+    // workgroup, 5.5 with 32 KB and 5.2 with 512 KB.
+    const int bytes = c.width * (c.dtype == F32 ? 4 : 2);
+    a.map = c.tokens ? (const uint8_t *)(space + w.map) : nullptr;
+    a.zero_lanes = 8;
+    while (a.zero_lanes < kThreads && a.zero_lanes * 16 < bytes) a.zero_lanes *= 2;
+    a.zero_rows = kThreads / a.zero_lanes;
+    while (a.zero_rows < 1024 && a.zero_rows * bytes < 16384) a.zero_rows *= 2;
+    const long long zeros = c.accumulate ? 0 : (c.vocab + a.zero_rows - 1) / a.zero_rows;
     return dispatch_embed(c, [&](auto dt, auto ot, auto nr, auto tiny) {
         const EmbedTable<nr.value> e = table_of<nr.value>(c);
         hipError_t st = hipSuccess;
@@ -512,7 +581,7 @@ hipError_t launch_embed_sum(const EmbedCall &c, const EmbedSpace &w, char *space
             st = launch(embed_sum_kernel<dt.value, ot.value, tiny.value, nr.value>, dim3((unsigned)(a.sums + zeros)),
                         dim3(kThreads), 0, s, e, a);
         if (st == hipSuccess && w.pieces > 1)
-            st = launch(embed_join_kernel<dt.value, nr.value>, dim3((unsigned)((w.pieces - 1) * a.slices)), dim3(kThreads), 0, s,
+            st = launch(embed_join_kernel<dt.value, kCols<dt.value, ot.value>, nr.value>, dim3((unsigned)((w.pieces - 1) * a.slices)), dim3(kThreads), 0, s,
                         e, a);
         return st;
     });

@@ -97,7 +97,7 @@ ar_status_t check_norm(const ar_norm_t *v, NormRow &r) {
     return AR_OK;
 }
 
-size_t norm_space(const ar_norm_t *v) { return (size_t)norm_back_groups(v->rows, (int)v->width) * v->width * sizeof(float); }
+size_t norm_space(const NormBackPlan &p) { return (size_t)p.groups * p.width * sizeof(float); }
 
 // ---- embedding ---------------------------------------------------------------
 ar_status_t check_embed(const ar_embed_t *v, EmbedCall &c) {
@@ -176,15 +176,31 @@ ar_status_t check_grad_buffers(const ar_grads_t *g, const void *const *bufs) {
     return AR_OK;
 }
 
+// Elements of a chunk, and whether the list stays in the 256 MB Infinity Cache.
+void grad_rule(const ar_grads_t *g, GradTable &t) {
+    long long all = 0, bytes = 0;
+    for (long long i = 0; i < g->count; ++i) all += g->sizes[i], bytes += g->sizes[i] * bytes_of(g->dtypes[i]);
+    t.chunk = kGradChunk;
+    while (t.chunk < kGradLongChunk && all > (long long)kGradGroups * t.chunk) t.chunk *= 2;
+    t.again = bytes <= 256LL << 20;
+}
+
 // Partial sums of a list at most: buffers that adjoin are taken as one, so there may be fewer.
 size_t grad_parts(const ar_grads_t *g) {
+    GradTable t;
+    grad_rule(g, t);
     long long entries = 0, chunks = 0;
     for (long long i = 0; i < g->count; ++i) {
         entries += (g->sizes[i] + kGradPieceMax - 1) / kGradPieceMax;
-        chunks += (g->sizes[i] + kGradChunk - 1) / kGradChunk;
+        chunks += (g->sizes[i] + t.chunk - 1) / t.chunk;
     }
     const long long launches = (entries + kGradTable - 1) / kGradTable;
     return (size_t)std::min(chunks, launches * kGradGroups);
+}
+// Workspace: the norm, the partial sums.
+size_t grad_space(const ar_grads_t *g) {
+    const size_t parts = grad_parts(g);
+    return parts ? (1 + parts) * sizeof(double) : 0;
 }
 
 // f(piece) for the list's buffers in turn, those that adjoin (in the outputs too) as one.
@@ -208,7 +224,10 @@ template <typename F> hipError_t each_piece(const ar_grads_t *g, void *const *ou
     return p.size ? f(p) : hipSuccess;
 }
 
-// f(table, chunks) for full tables of the list's pieces.
+// Chunks after which a table is launched: those of one more piece keep a grid's threads below 2^32.
+constexpr uint32_t kGradMostChunks = 1u << 22;
+
+// f(table, chunks) for full tables of the list's pieces, chunks of t.chunk elements or (0) of kGradScaleBytes.
 template <typename F> hipError_t each_table(const ar_grads_t *g, void *const *outs, GradTable &t, F &&f) {
     t.n = 0;
     t.first[0] = 0;
@@ -228,11 +247,12 @@ template <typename F> hipError_t each_table(const ar_grads_t *g, void *const *ou
             t.out[i] = p.out;
             t.size[i] = (uint32_t)size;
             t.dtype[i] = (uint8_t)p.dtype;
-            t.first[i + 1] = t.first[i] + (uint32_t)((size + kGradChunk - 1) / kGradChunk);
+            const long long chunk = t.chunk ? t.chunk : kGradScaleBytes / bytes_of(p.dtype);
+            t.first[i + 1] = t.first[i] + (uint32_t)((size + chunk - 1) / chunk);
             p.in += bytes;
             if (p.out) p.out += bytes;
             p.size -= size;
-            if (t.n == kGradTable) {
+            if (t.n == kGradTable || (!t.chunk && t.first[t.n] > kGradMostChunks)) {
                 const hipError_t e = flush();
                 if (e != hipSuccess) return e;
             }
@@ -247,6 +267,7 @@ int grad_groups(uint32_t chunks) { return (int)std::min<uint32_t>(chunks, kGradG
 // The launches that leave the list's partial sums in the workspace; how many there are goes into t.parts.
 hipError_t sum_squares(const ar_grads_t *g, void *const *outs, GradTable &t, double *part, hipStream_t stream) {
     int parts = 0;
+    grad_rule(g, t);
     const hipError_t e = each_table(g, outs, t, [&](GradTable &t, uint32_t chunks) {
         t.part = part + parts;
         parts += grad_groups(chunks);
@@ -280,7 +301,7 @@ ar_status_t ar_reduce_norm(const void *const *partials, const ar_norm_t *shape, 
     if (misaligned(weight, bytes_of(shape->weight_dtype)) || misaligned(residual, e) || misaligned(summed, e) ||
         misaligned(out, e) || misaligned(rstd, 4) || misaligned(scales, 4))
         return AR_ERR_ALIGNMENT;
-    c.a.group = shape->group / 8;
+    c.a.group = shape->group / (shape->dtype == AR_FLOAT32 ? 4 : 8);
     c.a.groups = shape->group ? (int)((shape->width + shape->group - 1) / shape->group) : 1;
 
     Span s[AR_MAX_RANKS + 8];
@@ -317,7 +338,7 @@ ar_status_t ar_norm_workspace(const ar_norm_t *shape, size_t *bytes) {
     if (!bytes) return AR_ERR_INVALID_ARG;
     const ar_status_t st = check_norm(shape, r);
     if (st != AR_OK) return st;
-    *bytes = norm_space(shape);
+    *bytes = norm_space(norm_back_plan(shape->dtype, shape->rows, (int)shape->width));
     return AR_OK;
 }
 
@@ -331,12 +352,13 @@ ar_status_t ar_reduce_norm_backward(const void *x, long long x_pitch, const ar_n
     if ((st = check_pitches(&x_pitch, 1, shape->width)) != AR_OK) return st;
     if (misaligned(grad_weight, 4)) return AR_ERR_ALIGNMENT;
     const long long e = bytes_of(shape->dtype), rows = shape->rows, row = shape->width * e;
+    const NormBackPlan plan = norm_back_plan(shape->dtype, rows, (int)shape->width);
     if (rows) {
         if (!x || !weight || !rstd || !grad_out || !grad_x) return AR_ERR_INVALID_ARG;
         if (misaligned(x, e) || misaligned(weight, bytes_of(shape->weight_dtype)) || misaligned(rstd, 4) ||
             misaligned(grad_out, e) || misaligned(grad_summed, e) || misaligned(grad_x, e))
             return AR_ERR_ALIGNMENT;
-        const size_t need = grad_weight ? norm_space(shape) : 0;
+        const size_t need = grad_weight ? norm_space(plan) : 0;
         if ((st = check_space(need, workspace, workspace_bytes)) != AR_OK) return st;
         Span s[8];
         int k = 0;
@@ -360,7 +382,8 @@ ar_status_t ar_reduce_norm_backward(const void *x, long long x_pitch, const ar_n
     a.grad_summed = (const char *)grad_summed;
     a.grad_x = (char *)grad_x;
     a.part = grad_weight ? (float *)workspace : nullptr;
-    return hip_status(launch_norm_back(shape->dtype, a, norm_back_groups(rows, (int)shape->width), grad_weight, stream));
+    a.part_width = plan.width;
+    return hip_status(launch_norm_back(shape->dtype, a, plan, grad_weight, stream));
 }
 
 ar_status_t ar_embedding(const void *const *tables, const ar_embed_t *shape, const int64_t *token_ids, void *out,
@@ -428,7 +451,7 @@ ar_status_t ar_grad_workspace(const ar_grads_t *grads, size_t *bytes) {
     if (!bytes) return AR_ERR_INVALID_ARG;
     const ar_status_t st = check_grads(grads);
     if (st != AR_OK) return st;
-    *bytes = grad_parts(grads) * sizeof(double);
+    *bytes = grad_space(grads);
     return AR_OK;
 }
 
@@ -439,7 +462,7 @@ ar_status_t ar_grad_norm(const ar_grads_t *grads, float scale, float *norm, void
     if (!(scale > 0.0f) || !std::isfinite(scale) || !norm) return AR_ERR_INVALID_ARG;
     if ((st = check_grad_buffers(grads, grads->bufs)) != AR_OK) return st;
     if (misaligned(norm, 4)) return AR_ERR_ALIGNMENT;
-    const size_t need = grad_parts(grads) * sizeof(double);
+    const size_t need = grad_space(grads);
     if ((st = check_space(need, workspace, workspace_bytes)) != AR_OK) return st;
     const uintptr_t n0 = (uintptr_t)norm, w0 = (uintptr_t)workspace;
     bool meets = need && n0 < w0 + need && w0 < n0 + 4;
@@ -450,7 +473,7 @@ ar_status_t ar_grad_norm(const ar_grads_t *grads, float scale, float *norm, void
     if (meets) return AR_ERR_INVALID_ARG;
     GradTable t{};
     t.scale = scale;
-    hipError_t e = sum_squares(grads, nullptr, t, (double *)workspace, stream);
+    hipError_t e = sum_squares(grads, nullptr, t, (double *)workspace + 1, stream);
     t.norm = norm;
     if (e == hipSuccess) e = launch_grad_finish(t, stream);
     return hip_status(e);
@@ -466,7 +489,7 @@ ar_status_t ar_clip_grads(const ar_grads_t *grads, void *const *outs, float max_
         (st = check_grad_buffers(grads, (const void *const *)outs)) != AR_OK)
         return st;
     if (misaligned(norm, 4)) return AR_ERR_ALIGNMENT;
-    const size_t need = grad_parts(grads) * sizeof(double);
+    const size_t need = grad_space(grads);
     if ((st = check_space(need, workspace, workspace_bytes)) != AR_OK) return st;
     {
         std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * grads->count + 2]);
@@ -486,12 +509,18 @@ ar_status_t ar_clip_grads(const ar_grads_t *grads, void *const *outs, float max_
     t.scale = scale;
     t.max_norm = max_norm;
     t.eps = eps;
-    hipError_t e = sum_squares(grads, outs, t, (double *)workspace, stream);
+    hipError_t e = sum_squares(grads, outs, t, (double *)workspace + 1, stream);
     t.norm = norm;
-    if (e == hipSuccess && t.parts == 0) e = launch_grad_finish(t, stream);
+    if (e == hipSuccess && (t.parts == 0 || t.parts > kGradInline)) {
+        t.wide = t.parts ? (double *)workspace : nullptr;
+        e = launch_grad_finish(t, stream);
+        t.parts = 0;
+        t.norm = nullptr;
+    }
+    t.chunk = 0;
     if (e == hipSuccess)
         e = each_table(grads, outs, t, [&](GradTable &t, uint32_t chunks) {
-            const hipError_t e = launch_grad_scale(t, grad_groups(chunks), stream);
+            const hipError_t e = launch_grad_scale(t, chunks, stream);
             t.norm = nullptr;
             return e;
         });

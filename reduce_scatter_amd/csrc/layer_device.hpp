@@ -1,7 +1,12 @@
 // layer_device.hpp -- device-side building blocks of the operators around a
-// step's collectives: runs of eight columns ("octs") in fp32, read and written
-// as 16-byte vectors at any element alignment, and sums over the lanes that
-// share a row.
+// step's collectives: runs of K columns per lane, in fp32, read and written as
+// vectors at any element alignment, and sums over the lanes that share a row.
+//
+// A run is the 16 bytes that one lane's store of the widest type involved takes
+// (8 columns of 16-bit elements, 4 where fp32 is written), so that the lanes of
+// a store instruction fill whole lines: with 8 fp32 columns to a lane, in two
+// stores that leave every other 16 bytes out, zeros were written at 2.2 TB/s
+// instead of 5.0.
 #pragma once
 
 #include "layer_kernels.hpp"
@@ -10,121 +15,139 @@
 namespace ar {
 
 typedef unsigned int u32x2e __attribute__((ext_vector_type(2), aligned(1)));   // 8 bytes at any alignment
+typedef unsigned int u32e __attribute__((aligned(1)));                         // 4 bytes at any alignment
 
-// Eight elements as stored.
-template <int DT> struct Oct {
-    u32x4 w[DT == F32 ? 2 : 1];
+// K elements as stored.
+template <int DT, int K> struct Run {
+    static constexpr int W = K * elem_bytes<DT>() / 4;
+    static_assert(W == 2 || W == 4 || W == 8, "8, 16 or 32 bytes");
+    uint32_t w[W];
 };
 
-template <int DT, bool STREAM = true> __device__ __forceinline__ Oct<DT> load_oct(const char *p) {
-    Oct<DT> o;
-    const u32x4e *q = (const u32x4e *)p;
+template <int DT, int K, bool STREAM = true> __device__ __forceinline__ Run<DT, K> load_run(const char *p) {
+    Run<DT, K> o;
+    if constexpr (o.W == 2) {
+        const u32x2e v = STREAM ? __builtin_nontemporal_load((const u32x2e *)p) : *(const u32x2e *)p;
+        o.w[0] = v[0], o.w[1] = v[1];
+    } else {
 #pragma unroll
-    for (int i = 0; i < (DT == F32 ? 2 : 1); ++i) o.w[i] = STREAM ? __builtin_nontemporal_load(q + i) : q[i];
+        for (int i = 0; i < o.W; i += 4) {
+            const u32x4e *q = (const u32x4e *)p + i / 4;
+            const u32x4e v = STREAM ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o.w[i + j] = v[j];
+        }
+    }
     return o;
 }
 
-// Fewer than eight elements (`left`), zeros behind them.
-template <int DT> __device__ __forceinline__ Oct<DT> load_short(const char *p, int left) {
-    Oct<DT> o;
+// Fewer than K elements (`left`), zeros behind them.
+template <int DT, int K> __device__ __forceinline__ Run<DT, K> load_short(const char *p, int left) {
+    Run<DT, K> o;
 #pragma unroll
-    for (int i = 0; i < (DT == F32 ? 2 : 1); ++i) o.w[i] = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < o.W; ++i) o.w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < K; ++i)
         if (i < left) {
-            if constexpr (DT == F32) o.w[i / 4][i % 4] = ((const uint32_t *)p)[i];
-            else o.w[0][i / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (i % 2));
+            if constexpr (DT == F32) o.w[i] = ((const uint32_t *)p)[i];
+            else o.w[i / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (i % 2));
         }
     return o;
 }
 
-template <int DT> __device__ __forceinline__ void widen(const Oct<DT> &o, float *v) {
-    constexpr int K = Pack<DT>::K;
+template <int DT, int K> __device__ __forceinline__ void widen(const Run<DT, K> &o, float *v) {
 #pragma unroll
-    for (int j = 0; j < 8 / K; ++j) {
-        const Pack<DT> p = unpack<DT>(o.w[j]);
-#pragma unroll
-        for (int i = 0; i < K; ++i) v[j * K + i] = p.v[i];
+    for (int i = 0; i < o.W; ++i) {
+        if constexpr (DT == F32) {
+            v[i] = bits_f32(o.w[i]);
+        } else if constexpr (DT == BF16) {
+            v[2 * i] = bits_f32(o.w[i] << 16);
+            v[2 * i + 1] = bits_f32(o.w[i] & 0xffff0000u);
+        } else {
+            v[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(o.w[i] & 0xffffu));
+            v[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(o.w[i] >> 16));
+        }
     }
 }
 
-// Eight values rounded once, to nearest even, to the storage type.
-template <int DT> __device__ __forceinline__ Oct<DT> narrow(const float *v) {
-    Oct<DT> o;
-    constexpr int K = Pack<DT>::K;
+// K values rounded once, to nearest even, to the storage type.
+template <int DT, int K> __device__ __forceinline__ Run<DT, K> narrow(const float *v) {
+    Run<DT, K> o;
 #pragma unroll
-    for (int j = 0; j < 8 / K; ++j) {
+    for (int i = 0; i < o.W; ++i) {
         if constexpr (DT == F32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o.w[j][i] = f32_bits(v[4 * j + i]);
+            o.w[i] = f32_bits(v[i]);
+        } else {
+            const f32x2 f = {fence_value(v[2 * i]), fence_value(v[2 * i + 1])};
+            if constexpr (DT == BF16) o.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+            else o.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+        }
+    }
+    return o;
+}
+
+// The first `left` elements (all from K on, none up to 0).
+template <int DT, int K, bool STREAM = true> __device__ __forceinline__ void store_run(char *p, const Run<DT, K> &o, int left) {
+    if (left >= K) {
+        if constexpr (Run<DT, K>::W == 2) {
+            const u32x2e v = {o.w[0], o.w[1]};
+            if constexpr (STREAM) __builtin_nontemporal_store(v, (u32x2e *)p);
+            else *(u32x2e *)p = v;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x2 f = {fence_value(v[2 * i]), fence_value(v[2 * i + 1])};
-                if constexpr (DT == BF16) o.w[j][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
-                else o.w[j][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+            for (int i = 0; i < o.W; i += 4) {
+                const u32x4e v = {o.w[i], o.w[i + 1], o.w[i + 2], o.w[i + 3]};
+                if constexpr (STREAM) __builtin_nontemporal_store(v, (u32x4e *)p + i / 4);
+                else *((u32x4e *)p + i / 4) = v;
             }
-        }
-    }
-    return o;
-}
-
-// The first `left` elements (all eight from 8 on, none up to 0).
-template <int DT, bool STREAM = true> __device__ __forceinline__ void store_oct(char *p, const Oct<DT> &o, int left) {
-    if (left >= 8) {
-        u32x4e *q = (u32x4e *)p;
-#pragma unroll
-        for (int i = 0; i < (DT == F32 ? 2 : 1); ++i) {
-            if constexpr (STREAM) __builtin_nontemporal_store((u32x4e)o.w[i], q + i);
-            else q[i] = o.w[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
+        for (int i = 0; i < K - 1; ++i)
             if (i < left) {
-                if constexpr (DT == F32) ((uint32_t *)p)[i] = o.w[i / 4][i % 4];
-                else ((uint16_t *)p)[i] = (uint16_t)(o.w[0][i / 2] >> (16 * (i % 2)));
+                if constexpr (DT == F32) ((uint32_t *)p)[i] = o.w[i];
+                else ((uint16_t *)p)[i] = (uint16_t)(o.w[i / 2] >> (16 * (i % 2)));
             }
     }
 }
 
 // v[i] = v[i + k], zeros from the end on (k >= 0).
-__device__ __forceinline__ void shift_down(float *v, int k) {
+template <int K> __device__ __forceinline__ void shift_down(float *v, int k) {
 #pragma unroll
-    for (int b = 4; b >= 1; b /= 2) {
+    for (int b = K / 2; b >= 1; b /= 2) {
         const bool on = k & b;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = on ? (i + b < 8 ? v[i + b] : 0.0f) : v[i];
+        for (int i = 0; i < K; ++i) v[i] = on ? (i + b < K ? v[i + b] : 0.0f) : v[i];
     }
-    if (k >= 8) {
+    if (k >= K) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < K; ++i) v[i] = 0.0f;
     }
 }
 
-// Where a lane's oct stands in its row.  A short last oct, and one behind the
-// row's end, is read as the row's last eight columns and moved into place, so
-// that no lane leaves the vector path; rows of fewer than eight columns (TINY)
-// are read by the element.
+// Where a lane's run stands in its row.  A short last run, and one behind the
+// row's end, is read as the row's last K columns and moved into place, so that
+// no lane leaves the vector path; rows of fewer than eight columns (TINY) are
+// read by the element.
 struct ColPlace {
     int col, at, left;                 // first column, the column read from, columns from col on
 };
-template <bool TINY> __device__ __forceinline__ ColPlace col_place(int oct, int width) {
+template <int K, bool TINY> __device__ __forceinline__ ColPlace col_place(int run, int width) {
     ColPlace p;
-    p.col = oct * 8;
+    p.col = run * K;
     p.left = width - p.col;
-    p.at = TINY ? 0 : (p.left >= 8 ? p.col : width - 8);
+    p.at = TINY ? 0 : (p.left >= K ? p.col : width - K);
     return p;
 }
-template <int DT, bool TINY, bool STREAM = true>
-__device__ __forceinline__ Oct<DT> load_at(const char *row, const ColPlace &p) {
-    if constexpr (TINY) return load_short<DT>(row, p.col == 0 ? p.left : 0);
-    else return load_oct<DT, STREAM>(row + (long long)p.at * elem_bytes<DT>());
+template <int DT, int K, bool TINY, bool STREAM = true>
+__device__ __forceinline__ Run<DT, K> load_at(const char *row, const ColPlace &p) {
+    if constexpr (TINY) return load_short<DT, K>(row + (p.left > 0 ? p.col * elem_bytes<DT>() : 0), p.left);
+    else return load_run<DT, K, STREAM>(row + (long long)p.at * elem_bytes<DT>());
 }
 // Into place, and zeros behind the row's end.
-template <bool TINY> __device__ __forceinline__ void settle(float *v, const ColPlace &p) {
+template <int K, bool TINY> __device__ __forceinline__ void settle(float *v, const ColPlace &p) {
     if constexpr (!TINY)
-        if (p.left < 8) shift_down(v, p.col - p.at);
+        if (p.left < K) shift_down<K>(v, p.col - p.at);
 }
 
 // Sum (largest bits) over the LANES lanes of a row within a wave.

@@ -27,7 +27,7 @@ template <int NR> struct NormArgs {
     const char *x[NR];                 // partials
     uint32_t pitch[NR];                // elements between rows
     int n;
-    int group;                         // lanes of 8 columns that share a scale; 0: the row
+    int group;                         // runs that share a scale; 0: the row
     int groups;                        // scales of a row
     NormRow r;
     const char *residual;
@@ -44,7 +44,8 @@ struct NormBackArgs {
     const float *rstd;
     const char *grad_out, *grad_summed;
     char *grad_x;
-    float *part;                       // [workgroups, width] partial weight gradients; NULL: none wanted
+    float *part;                       // [workgroups, part_width] partial weight gradients; NULL: none wanted
+    int part_width;
 };
 
 // Host-side description of a forward launch, rank tables of any size.
@@ -56,9 +57,12 @@ struct NormCall {
 };
 
 hipError_t launch_reduce_norm(const NormCall &c, hipStream_t s);
-// Workgroups of the backward pass, one partial weight gradient each.
-int norm_back_groups(long long rows, int width);
-hipError_t launch_norm_back(int dtype, const NormBackArgs &a, int groups, float *grad_weight, hipStream_t s);
+// Workgroups of the backward pass, and the places of the partial weight gradient that each leaves.
+struct NormBackPlan {
+    int groups, width;
+};
+NormBackPlan norm_back_plan(int dtype, long long rows, int width);
+hipError_t launch_norm_back(int dtype, const NormBackArgs &a, const NormBackPlan &plan, float *grad_weight, hipStream_t s);
 
 // ---- embedding ---------------------------------------------------------------
 template <int NR> struct EmbedTable {
@@ -88,7 +92,7 @@ struct EmbedSorted {
 
 // Pieces of the backward pass's workspace.
 struct EmbedSpace {
-    size_t keys, order, keys2, order2, hist, totals, part, bytes;
+    size_t keys, order, map, keys2, order2, hist, totals, part, bytes;
     int piece;                         // sorted positions to a workgroup
     long long pieces;
     int digit, passes;                 // bits of a counting pass, and how many (0: ranked in one launch)
@@ -103,8 +107,12 @@ hipError_t launch_embed_sum(const EmbedCall &c, const EmbedSpace &w, char *space
 
 // ---- gradient norm -----------------------------------------------------------
 constexpr int kGradTable = 120;        // buffers of a launch
-constexpr int kGradChunk = 16384;      // elements that a workgroup takes at a time
-constexpr int kGradGroups = 1024;      // most workgroups, one partial sum each, of a launch
+constexpr int kGradChunk = 4096;       // elements that a workgroup takes at a time, doubled while there are more chunks than
+constexpr int kGradLongChunk = 65536;  // workgroups, up to this
+constexpr int kGradGroups = 4096;      // most workgroups, one partial sum each, of a launch
+
+constexpr int kGradScaleBytes = 8192;  // that a workgroup scales
+constexpr int kGradInline = 256;       // most partial sums that every workgroup of the scaling launch adds up by itself
 
 struct GradPiece {                     // buffers that adjoin, as one
     const char *in;
@@ -120,17 +128,20 @@ struct GradTable {
     uint32_t first[kGradTable + 1];    // first chunk; all chunks from first[n] on
     uint8_t dtype[kGradTable];
     int n;
+    int chunk;                         // elements, kGradChunk to kGradLongChunk
+    bool again;                        // what is read for the norm stays in the cache for the scaling
     double *part;                      // of this launch (sums) or of all launches (scaling)
-    int parts;                         // partial sums of all launches
+    int parts;                         // partial sums of all launches; 0 (scaling): `wide` holds the norm
     float scale, max_norm, eps;
     float *norm;                       // where the norm is written, by one launch
+    double *wide;                      // the norm in 64 bits
 };
 
 // Most elements of a table entry, whole chunks (larger buffers are cut).
-constexpr long long kGradPieceMax = (1LL << 32) - kGradChunk;
+constexpr long long kGradPieceMax = (1LL << 32) - kGradLongChunk;
 
 hipError_t launch_grad_sum(const GradTable &t, int groups, hipStream_t s);
 hipError_t launch_grad_finish(const GradTable &t, hipStream_t s);
-hipError_t launch_grad_scale(const GradTable &t, int groups, hipStream_t s);
+hipError_t launch_grad_scale(const GradTable &t, uint32_t groups, hipStream_t s);
 
 }  // namespace ar

@@ -6,9 +6,9 @@
 //   h = x rstd, u = g (offset + w),  dx = rstd (u - h mean(u h)) + g_s,  dw = sum over rows of g h
 //
 // Both are bounded by HBM bytes: a row is read once, stays in registers between
-// its sum and its results, and is written once.  A row of up to 128 columns
-// belongs to 16 lanes, one of up to 512 to a wave, a longer one to a workgroup
-// of as many waves as it needs.
+// its sum and its results, and is written once.  A row of up to 16 runs (16
+// bytes each) belongs to 16 lanes, one of up to 64 to a wave, a longer one to a
+// workgroup of as many waves as it needs.
 #include "dispatch.hpp"
 #include "layer_device.hpp"
 
@@ -43,32 +43,32 @@ template <int LANES> __device__ __forceinline__ uint32_t row_max(uint32_t v, uin
 }
 
 // offset + weight of a lane's columns.
-template <int DT, bool TINY> __device__ __forceinline__ void load_weight(const NormRow &r, const ColPlace &p, float *w) {
-    if (r.weight32) widen<F32>(load_at<F32, TINY, false>((const char *)r.weight, p), w);
-    else widen<DT>(load_at<DT, TINY, false>((const char *)r.weight, p), w);
-    settle<TINY>(w, p);
+template <int DT, int K, bool TINY> __device__ __forceinline__ void load_weight(const NormRow &r, const ColPlace &p, float *w) {
+    if (r.weight32) widen<F32, K>(load_at<F32, K, TINY, false>((const char *)r.weight, p), w);
+    else widen<DT, K>(load_at<DT, K, TINY, false>((const char *)r.weight, p), w);
+    settle<K, TINY>(w, p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] += r.offset;
+    for (int i = 0; i < K; ++i) w[i] += r.offset;
 }
 
 // Adds ranks r, ..., r + B - 1, their loads issued together.
-template <int B, int DT, int U, bool TINY, int NR>
-__device__ __forceinline__ void add_ranks(const NormArgs<NR> &a, int r, long long row, const ColPlace *p, float (*s)[8]) {
-    Oct<DT> o[B][U];
+template <int B, int DT, int K, int U, bool TINY, int NR>
+__device__ __forceinline__ void add_ranks(const NormArgs<NR> &a, int r, long long row, const ColPlace *p, float (*s)[K]) {
+    Run<DT, K> o[B][U];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
         const char *x = a.x[r + b] + row * (long long)a.pitch[r + b] * elem_bytes<DT>();
 #pragma unroll
-        for (int u = 0; u < U; ++u) o[b][u] = load_at<DT, TINY>(x, p[u]);
+        for (int u = 0; u < U; ++u) o[b][u] = load_at<DT, K, TINY>(x, p[u]);
     }
 #pragma unroll
     for (int b = 0; b < B; ++b)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float v[8];
-            widen<DT>(o[b][u], v);
+            float v[K];
+            widen<DT, K>(o[b][u], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[u][i] += v[i];
+            for (int i = 0; i < K; ++i) s[u][i] += v[i];
         }
 }
 
@@ -76,7 +76,8 @@ template <int DT, int U, int LANES, bool TINY, int NR>
 __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduce_norm_kernel(const NormArgs<NR> a) {
     __shared__ float lds_sum[kNormWaves];
     __shared__ double lds_wide[kNormWaves];
-    __shared__ uint32_t lds_max[kNormWaves];
+    __shared__ uint32_t lds_max[kNormWaves * U];
+    constexpr int K = Lanes<DT>::value;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int threads = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
     const int width = a.r.width;
@@ -85,36 +86,36 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
     if (LANES && row >= a.r.rows) return;
 
     ColPlace p[U];
-    float s[U][8];
+    float s[U][K];
 #pragma unroll
-    for (int u = 0; u < U; ++u) p[u] = col_place<TINY>(u * threads + t, width);
+    for (int u = 0; u < U; ++u) p[u] = col_place<K, TINY>(u * threads + t, width);
     const long long packed = row * width;          // of the tensors without a pitch
     if (a.residual) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) widen<DT>(load_at<DT, TINY>(a.residual + packed * elem_bytes<DT>(), p[u]), s[u]);
+        for (int u = 0; u < U; ++u) widen<DT, K>(load_at<DT, K, TINY>(a.residual + packed * elem_bytes<DT>(), p[u]), s[u]);
     } else {
         // -0 + x is x for every x, a negative zero included
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[u][i] = -0.0f;
+            for (int i = 0; i < K; ++i) s[u][i] = -0.0f;
     }
-    constexpr int B = (DT == F32 ? 4 : 8) / U;
+    constexpr int B = 8 / U;
     int r = 0;
-    for (; r + B <= a.n; r += B) add_ranks<B, DT, U, TINY>(a, r, row, p, s);
+    for (; r + B <= a.n; r += B) add_ranks<B, DT, K, U, TINY>(a, r, row, p, s);
     if constexpr (B > 4)
-        if (r + 4 <= a.n) add_ranks<4, DT, U, TINY>(a, r, row, p, s), r += 4;
+        if (r + 4 <= a.n) add_ranks<4, DT, K, U, TINY>(a, r, row, p, s), r += 4;
     if constexpr (B > 2)
-        if (r + 2 <= a.n) add_ranks<2, DT, U, TINY>(a, r, row, p, s), r += 2;
+        if (r + 2 <= a.n) add_ranks<2, DT, K, U, TINY>(a, r, row, p, s), r += 2;
     if constexpr (B > 1)
-        if (r < a.n) add_ranks<1, DT, U, TINY>(a, r, row, p, s);
+        if (r < a.n) add_ranks<1, DT, K, U, TINY>(a, r, row, p, s);
 
     float sq = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        settle<TINY>(s[u], p[u]);
+        settle<K, TINY>(s[u], p[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(s[u][i], s[u][i], sq);
+        for (int i = 0; i < K; ++i) sq = __builtin_fmaf(s[u][i], s[u][i], sq);
     }
     sq = row_sum<LANES>(sq, lds_sum, waves, wave, lane);
     float rstd;
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) wide = __builtin_fma((double)s[u][i], (double)s[u][i], wide);
+            for (int i = 0; i < K; ++i) wide = __builtin_fma((double)s[u][i], (double)s[u][i], wide);
         wide = row_sum<LANES>(wide, lds_wide, waves, wave, lane);
         rstd = (float)(1.0 / __builtin_sqrt(wide / width + (double)a.r.eps));
     }
@@ -135,20 +136,20 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
     if (a.summed) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            store_oct<DT>(a.summed + (packed + p[u].col) * elem_bytes<DT>(), narrow<DT>(s[u]), p[u].left);
+            store_run<DT, K>(a.summed + (packed + p[u].col) * elem_bytes<DT>(), narrow<DT, K>(s[u]), p[u].left);
     }
     if (!a.out && !a.out8) return;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float w[8];
-        load_weight<DT, TINY>(a.r, p[u], w);
+        float w[K];
+        load_weight<DT, K, TINY>(a.r, p[u], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[u][i] = p[u].left > i ? s[u][i] * rstd * w[i] : 0.0f;
+        for (int i = 0; i < K; ++i) s[u][i] = p[u].left > i ? s[u][i] * rstd * w[i] : 0.0f;
     }
     if (a.out) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            store_oct<DT>(a.out + (packed + p[u].col) * elem_bytes<DT>(), narrow<DT>(s[u]), p[u].left);
+            store_run<DT, K>(a.out + (packed + p[u].col) * elem_bytes<DT>(), narrow<DT, K>(s[u]), p[u].left);
     }
     if (!a.out8) return;
 
@@ -159,162 +160,197 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
     for (int u = 0; u < U; ++u) {
         most[u] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < K; ++i) {
             const uint32_t b = f32_bits(s[u][i]) & 0x7fffffffu;
             most[u] = b > most[u] ? b : most[u];
         }
         all = most[u] > all ? most[u] : all;
     }
-    if (a.group == 0) all = row_max<LANES>(all, lds_max, waves, wave, lane);
+    if (a.group == 0) {
+        all = row_max<LANES>(all, lds_max, waves, wave, lane);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (a.group == 0) {
-            most[u] = all;
-        } else {
+        for (int u = 0; u < U; ++u) most[u] = all;
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
             row_bits<kWaveLanes<LANES>>([&](auto m) {
                 if (m.value < a.group) {
                     const uint32_t o = lane_xor<m.value>(most[u], lane);
                     most[u] = o > most[u] ? o : most[u];
                 }
             });
+        if (LANES == 0 && a.group > 64) {
+            // a group of 512 columns in fp32: those of two neighbouring waves, in the order of the row
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (lane == 0) lds_max[u * waves + wave] = most[u];
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int other = (u * waves + wave) ^ 1;
+                if (other < U * waves) most[u] = lds_max[other] > most[u] ? lds_max[other] : most[u];
+            }
         }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
         const float amax = bits_f32(most[u]);
         const bool fine = finite(amax);
         const float scale = fine ? __builtin_fmaxf(amax / kE4m3Max, kLeastScale) : bits_f32(0x7fc00000u);
         const float inv = 1.0f / scale;
-        const bool first = a.group ? t % a.group == 0 : (t == 0 && u == 0);
-        if (first && p[u].left > 0) a.scales[row * a.groups + (a.group ? p[u].col / (8 * a.group) : 0)] = scale;
-        uint32_t q[2];
+        const int run = u * threads + t;
+        if (p[u].left > 0 && (a.group ? run % a.group == 0 : run == 0)) a.scales[row * a.groups + (a.group ? run / a.group : 0)] = scale;
+        uint32_t q[K / 4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < K / 4; ++i) {
             int v = __builtin_amdgcn_cvt_pk_fp8_f32(s[u][4 * i] * inv, s[u][4 * i + 1] * inv, 0, false);
             v = __builtin_amdgcn_cvt_pk_fp8_f32(s[u][4 * i + 2] * inv, s[u][4 * i + 3] * inv, v, true);
             q[i] = fine ? (uint32_t)v : 0x7f7f7f7fu;
         }
         uint8_t *to = a.out8 + packed + p[u].col;
-        if (p[u].left >= 8) {
-            __builtin_nontemporal_store(u32x2e{q[0], q[1]}, (u32x2e *)to);
+        if (p[u].left >= K) {
+            if constexpr (K == 8) __builtin_nontemporal_store(u32x2e{q[0], q[1]}, (u32x2e *)to);
+            else __builtin_nontemporal_store(q[0], (u32e *)to);
         } else {
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
+            for (int i = 0; i < K - 1; ++i)
                 if (i < p[u].left) to[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
         }
     }
 }
 
 // h = x rstd and u = g (offset + w) of a lane's columns; g as it came.
-template <int DT, bool TINY>
-__device__ __forceinline__ void back_terms(const Oct<DT> &xo, const Oct<DT> &go, const ColPlace &p, const float *w,
+template <int DT, int K, bool TINY>
+__device__ __forceinline__ void back_terms(const Run<DT, K> &xo, const Run<DT, K> &go, const ColPlace &p, const float *w,
                                            float rstd, float *h, float *g, float *u) {
-    widen<DT>(xo, h);
-    widen<DT>(go, g);
-    settle<TINY>(h, p);
-    settle<TINY>(g, p);
+    widen<DT, K>(xo, h);
+    widen<DT, K>(go, g);
+    settle<K, TINY>(h, p);
+    settle<K, TINY>(g, p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < K; ++i) {
         h[i] *= rstd;
         u[i] = g[i] * w[i];
     }
 }
 
-// A workgroup takes every gridDim.x-th set of rows and keeps its part of the
-// weight's gradient in registers throughout, and the weight too while that is
-// eight columns to a lane.
+template <int DT, int K, int U> struct BackRow {       // a row as stored
+    Run<DT, K> x[U], g[U], s[U];
+    float rstd;
+};
+template <int DT, int K, int U, bool TINY>
+__device__ __forceinline__ void load_back(const NormBackArgs &a, long long row, const ColPlace *p, BackRow<DT, K, U> &o) {
+    const long long packed = row * a.r.width * elem_bytes<DT>();
+    const char *x = a.x + row * a.x_pitch * elem_bytes<DT>();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        o.x[u] = load_at<DT, K, TINY>(x, p[u]);
+        o.g[u] = load_at<DT, K, TINY>(a.grad_out + packed, p[u]);
+        if (a.grad_summed) o.s[u] = load_at<DT, K, TINY>(a.grad_summed + packed, p[u]);
+    }
+    o.rstd = a.rstd[row];
+}
+
+// A workgroup takes every gridDim.x-th set of rows, the next one's loads in
+// flight while it works on one, and keeps its part of the weight's gradient in
+// registers throughout, and the weight too while that is one run to a lane.
 template <int DT, int U, int LANES, bool TINY>
 __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void norm_back_kernel(const NormBackArgs a) {
+    constexpr int K = Lanes<DT>::value;
     constexpr int kSets = LANES ? kShortThreads / (LANES ? LANES : 1) : 1;     // rows at a time
     __shared__ float lds_sum[2][kNormWaves];
-    __shared__ float lds_part[LANES ? kShortThreads / 64 : 1][LANES ? 512 : 1];
+    __shared__ float lds_part[LANES ? kShortThreads / 64 : 1][LANES ? 64 * K : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int threads = LANES ? LANES : blockDim.x, t = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
     const int width = a.r.width;
     ColPlace p[U];
-    float w[8], dw[U][8];
+    float w[K], dw[U][K];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        p[u] = col_place<TINY>(u * threads + t, width);
+        p[u] = col_place<K, TINY>(u * threads + t, width);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
+        for (int i = 0; i < K; ++i) dw[u][i] = 0.0f;
     }
-    if constexpr (U == 1) load_weight<DT, TINY>(a.r, p[0], w);
-    int flip = 0;
-    for (long long row = (long long)blockIdx.x * kSets + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0); row < a.r.rows;
-         row += (long long)gridDim.x * kSets, flip ^= 1) {
-        const long long packed = row * width * elem_bytes<DT>();
-        const char *xr = a.x + row * a.x_pitch * elem_bytes<DT>();
-        Oct<DT> xo[U], go[U], so[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) xo[u] = load_at<DT, TINY>(xr, p[u]), go[u] = load_at<DT, TINY>(a.grad_out + packed, p[u]);
-        if (a.grad_summed) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) so[u] = load_at<DT, TINY>(a.grad_summed + packed, p[u]);
+    constexpr bool kAhead = U * K <= 8;            // longer rows have no registers for a second one
+    const long long step = (long long)gridDim.x * kSets;
+    long long row = (long long)blockIdx.x * kSets + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
+    BackRow<DT, K, U> next;
+    if (kAhead && row < a.r.rows) load_back<DT, K, U, TINY>(a, row, p, next);
+    if constexpr (U == 1) load_weight<DT, K, TINY>(a.r, p[0], w);
+    for (int flip = 0; row < a.r.rows; row += step, flip ^= 1) {
+        BackRow<DT, K, U> o;
+        if constexpr (kAhead) {
+            o = next;
+            if (row + step < a.r.rows) load_back<DT, K, U, TINY>(a, row + step, p, next);
+        } else {
+            load_back<DT, K, U, TINY>(a, row, p, o);
         }
-        const float rstd = a.rstd[row];
-        float h[8], g[8], uv[8], dot = 0.0f;
+        float h[K], g[K], uv[K], dot = 0.0f;
         NormRow again = a.r;           // longer rows: read where it is used, not kept across rows
         if constexpr (U > 1) asm volatile("" : "+s"(again.weight));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if constexpr (U > 1) {
-                __builtin_amdgcn_sched_barrier(0);     // one oct's terms at a time
-                load_weight<DT, TINY>(again, p[u], w);
-            }
-            back_terms<DT, TINY>(xo[u], go[u], p[u], w, rstd, h, g, uv);
+            if constexpr (U > 1) load_weight<DT, K, TINY>(again, p[u], w);
+            back_terms<DT, K, TINY>(o.x[u], o.g[u], p[u], w, o.rstd, h, g, uv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < K; ++i) {
                 dw[u][i] = __builtin_fmaf(g[i], h[i], dw[u][i]);
                 if (p[u].left > i) dot = __builtin_fmaf(uv[i], h[i], dot);
             }
         }
-        if (a.grad_summed) {
-            // grad_x may be one of the inputs, and a short oct is read from columns that another lane writes:
-            // everything has been read before the sum's barrier
+        // grad_x may be one of the inputs, and a short run is read from columns that another lane writes: everything of
+        // the row has been read before the sum's barrier.  Longer rows work the terms out again from the values as
+        // stored, which take half the registers.
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < (DT == F32 ? 2 : 1); ++j) asm volatile("" : "+v"(so[u].w[j]));
-        }
+            for (int j = 0; j < o.x[u].W; ++j) {
+                if (a.grad_summed) asm volatile("" : "+v"(o.s[u].w[j]));
+            }
         const float c = row_sum<LANES>(dot, lds_sum[flip], waves, wave, lane) / (float)width;
         if constexpr (U > 1) {
-            // longer rows: the terms are worked out again from the values as stored, which take half the registers
             asm volatile("" : "+s"(again.weight));
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < (DT == F32 ? 2 : 1); ++j) asm volatile("" : "+v"(xo[u].w[j]), "+v"(go[u].w[j]));
+                for (int j = 0; j < o.x[u].W; ++j) asm volatile("" : "+v"(o.x[u].w[j]), "+v"(o.g[u].w[j]));
         }
+        char *to = a.grad_x + row * width * elem_bytes<DT>();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (U > 1) {
-                __builtin_amdgcn_sched_barrier(0);
-                load_weight<DT, TINY>(again, p[u], w);
-                back_terms<DT, TINY>(xo[u], go[u], p[u], w, rstd, h, g, uv);
+                load_weight<DT, K, TINY>(again, p[u], w);
+                back_terms<DT, K, TINY>(o.x[u], o.g[u], p[u], w, o.rstd, h, g, uv);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) uv[i] = rstd * __builtin_fmaf(-h[i], c, uv[i]);
+            for (int i = 0; i < K; ++i) uv[i] = o.rstd * __builtin_fmaf(-h[i], c, uv[i]);
             if (a.grad_summed) {
-                widen<DT>(so[u], g);
-                settle<TINY>(g, p[u]);
+                widen<DT, K>(o.s[u], g);
+                settle<K, TINY>(g, p[u]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) uv[i] += g[i];
+                for (int i = 0; i < K; ++i) uv[i] += g[i];
             }
-            store_oct<DT>(a.grad_x + packed + (long long)p[u].col * elem_bytes<DT>(), narrow<DT>(uv), p[u].left);
+            store_run<DT, K>(to + (long long)p[u].col * elem_bytes<DT>(), narrow<DT, K>(uv), p[u].left);
         }
     }
     if (!a.part) return;
-    float *part = a.part + (long long)blockIdx.x * width;
+    float *part = a.part + (long long)blockIdx.x * a.part_width;
     if constexpr (LANES == 0) {
+        // four columns of every lane after the other, so that a store's lanes fill whole lines
 #pragma unroll
-        for (int u = 0; u < U; ++u) store_oct<F32, false>((char *)(part + p[u].col), narrow<F32>(dw[u]), p[u].left);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < K / 4; ++j)
+                store_run<F32, 4, false>((char *)(part + ((u * (K / 4) + j) * threads + t) * 4), narrow<F32, 4>(dw[u] + 4 * j), 4);
     } else {
         // rows of one workgroup, first within a wave (LANES 16), then over its waves
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < K; ++i) {
             if constexpr (LANES == 16) {
                 dw[0][i] += bits_f32(lane_xor<16>(f32_bits(dw[0][i]), lane));
                 dw[0][i] += bits_f32(lane_xor<32>(f32_bits(dw[0][i]), lane));
             }
-            if (lane < LANES) lds_part[wave][lane * 8 + i] = dw[0][i];
+            if (lane < LANES) lds_part[wave][lane * K + i] = dw[0][i];
         }
         __syncthreads();
         for (int col = threadIdx.x; col < width; col += kShortThreads) {
@@ -325,36 +361,56 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void norm_
     }
 }
 
-// Sum of the workgroups' partial weight gradients: 16 columns by 16 slices of the workgroups.
-__global__ __launch_bounds__(256) void norm_weight_kernel(const float *part, int groups, int width, float *out) {
-    __shared__ float lds[16][17];
-    const int c = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+// Sum of the workgroups' partial weight gradients: 64 places by 16 slices of the
+// workgroups.  `quads` is the number of lanes whose four columns follow one
+// another in a partial gradient, `per` how many fours a lane has in a row (0:
+// the columns are in order).
+constexpr int kWeightSlices = 16;
+__global__ __launch_bounds__(64 * kWeightSlices) void norm_weight_kernel(const float *part, int groups, int part_width, int quads,
+                                                                         int per, int width, float *out) {
+    __shared__ float lds[kWeightSlices][64];
+    const int c = threadIdx.x & 63, k = threadIdx.x >> 6, at = blockIdx.x * 64 + c;
     float v = 0.0f;
-    if (col < width)
-        for (int g = k; g < groups; g += 16) v += part[(long long)g * width + col];
+    if (at < part_width) {
+        constexpr int B = 8;
+        int g = k;
+        for (; g + (B - 1) * kWeightSlices < groups; g += B * kWeightSlices) {
+            float f[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) f[b] = part[(long long)(g + b * kWeightSlices) * part_width + at];
+#pragma unroll
+            for (int b = 0; b < B; ++b) v += f[b];
+        }
+        for (; g < groups; g += kWeightSlices) v += part[(long long)g * part_width + at];
+    }
     lds[k][c] = v;
     __syncthreads();
-    if (k == 0 && col < width) {
-        v = 0.0f;
-        for (int i = 0; i < 16; ++i) v += lds[i][c];
-        out[col] = v;
+    if (k != 0 || at >= part_width) return;
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWeightSlices; ++i) v += lds[i][c];
+    int col = at;
+    if (per) {
+        const int four = at / 4 / quads, lane = at / 4 % quads;
+        col = ((four / per * quads + lane) * per + four % per) * 4 + at % 4;
     }
+    if (col < width) out[col] = v;
 }
 
-// Lanes, octs per lane and waves of a row.
+// Lanes, runs per lane and threads of a row.
 struct RowPlan {
     int lanes, u, threads;
 };
-RowPlan plan_row(int width) {
-    const int octs = (width + 7) / 8;
-    if (octs <= 16) return {16, 1, kShortThreads};
-    if (octs <= 64) return {64, 1, kShortThreads};
+RowPlan plan_row(int dtype, int width) {
+    const int k = dtype == F32 ? 4 : 8, runs = (width + k - 1) / k;
+    if (runs <= 16) return {16, 1, kShortThreads};
+    if (runs <= 64) return {64, 1, kShortThreads};
     int u = 1;
-    while (octs > 64 * kNormWaves * u) u *= 2;
-    return {0, u, (octs + 64 * u - 1) / (64 * u) * 64};
+    while (runs > 64 * kNormWaves * u) u *= 2;
+    return {0, u, (runs + 64 * u - 1) / (64 * u) * 64};
 }
 
-// f(dtype, octs per lane, lanes of a row, whether rows are shorter than an oct)
+// f(dtype, runs per lane, lanes of a row, whether rows are shorter than eight columns)
 template <typename F> hipError_t dispatch_rows(int dtype, const RowPlan &p, int width, F &&f) {
     auto by_dt = [&](auto dt) {
         constexpr std::integral_constant<int, 1> one{};
@@ -362,11 +418,10 @@ template <typename F> hipError_t dispatch_rows(int dtype, const RowPlan &p, int 
         if (p.lanes == 16) return f(dt, one, std::integral_constant<int, 16>{}, std::false_type{});
         if (p.lanes == 64) return f(dt, one, std::integral_constant<int, 64>{}, std::false_type{});
         constexpr std::integral_constant<int, 0> block{};
-        switch (p.u) {
-        case 1: return f(dt, one, block, std::false_type{});
-        case 2: return f(dt, std::integral_constant<int, 2>{}, block, std::false_type{});
-        default: return hipErrorInvalidValue;
-        }
+        if (p.u == 1) return f(dt, one, block, std::false_type{});
+        if (p.u == 2) return f(dt, std::integral_constant<int, 2>{}, block, std::false_type{});
+        if constexpr (dt.value == F32) return f(dt, std::integral_constant<int, 4>{}, block, std::false_type{});
+        return hipErrorInvalidValue;
     };
     switch (dtype) {
     case F32: return by_dt(std::integral_constant<int, F32>{});
@@ -408,31 +463,31 @@ hipError_t launch_forward(const NormCall &c, const RowPlan &p, DT, U, L, T, hipS
 }  // namespace
 
 hipError_t launch_reduce_norm(const NormCall &c, hipStream_t s) {
-    const RowPlan p = plan_row(c.a.r.width);
+    const RowPlan p = plan_row(c.dtype, c.a.r.width);
     return dispatch_rows(c.dtype, p, c.a.r.width, [&](auto dt, auto u, auto l, auto tiny) {
         return c.n <= kLayerFew ? launch_forward<kLayerFew>(c, p, dt, u, l, tiny, s)
                                 : launch_forward<kLayerMany>(c, p, dt, u, l, tiny, s);
     });
 }
 
-int norm_back_groups(long long rows, int width) {
-    const RowPlan p = plan_row(width);
+NormBackPlan norm_back_plan(int dtype, long long rows, int width) {
+    const RowPlan p = plan_row(dtype, width);
     const long long sets = p.lanes ? kShortThreads / p.lanes : 1;
-    const long long groups = (rows + sets - 1) / sets, most = 256LL * (2048 / p.threads);
-    return (int)(groups < most ? groups : most);
+    const long long groups = (rows + sets - 1) / sets, most = 256LL * (p.lanes ? 8 : 1024 / p.threads);
+    return {(int)(groups < most ? groups : most), p.lanes ? width : p.u * (dtype == F32 ? 4 : 8) * p.threads};
 }
 
-hipError_t launch_norm_back(int dtype, const NormBackArgs &a, int groups, float *grad_weight, hipStream_t s) {
-    const RowPlan p = plan_row(a.r.width);
+hipError_t launch_norm_back(int dtype, const NormBackArgs &a, const NormBackPlan &plan, float *grad_weight, hipStream_t s) {
+    const RowPlan p = plan_row(dtype, a.r.width);
     hipError_t e = hipSuccess;
-    if (groups)
+    if (plan.groups)
         e = dispatch_rows(dtype, p, a.r.width, [&](auto dt, auto u, auto l, auto tiny) {
-            return launch(norm_back_kernel<dt.value, u.value, l.value, tiny.value>, dim3((unsigned)groups),
+            return launch(norm_back_kernel<dt.value, u.value, l.value, tiny.value>, dim3((unsigned)plan.groups),
                           dim3((unsigned)p.threads), 0, s, a);
         });
     if (e == hipSuccess && grad_weight)
-        e = launch(norm_weight_kernel, dim3((unsigned)((a.r.width + 15) / 16)), dim3(256), 0, s, (const float *)a.part, groups,
-                   a.r.width, grad_weight);
+        e = launch(norm_weight_kernel, dim3((unsigned)((plan.width + 63) / 64)), dim3(64 * kWeightSlices), 0, s, (const float *)a.part,
+                   plan.groups, plan.width, p.threads, p.lanes ? 0 : dtype == F32 ? 1 : 2, a.r.width, grad_weight);
     return e;
 }
 
