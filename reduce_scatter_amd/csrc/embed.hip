@@ -82,23 +82,32 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, int vocab) {
 }
 
 // Few tokens: a token's place is the number of those before it in the order,
-// (key, position) being compared, counted directly.  A wave counts for eight
-// tokens at once against 64 tokens a step.  The workgroups behind those write
-// which entries have a token, kMapEach of them each.
+// (key, position) being compared, counted directly.  A workgroup counts for
+// eight tokens, its waves dealing out the steps of 64 tokens that these are
+// compared with.  The workgroups behind those write which entries have a token,
+// kMapEach of them each.
+// The whole gradient of 64 columns, 50000 entries, by counting (by passes over
+// digits), us: 1024 tokens 16.8 (28.4), 4096 19.9 (30.2), 8192 26.4 (31.5), 12288
+// 35.8 (32.1), 16384 47.6 (34.5).
+constexpr long long kRankTokens = 10240;
 constexpr int kRankEach = 8;
 constexpr int kMapEach = 1024;
 __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids, int tokens, int vocab, uint32_t *keys,
                                                               uint32_t *order, uint8_t *map, int ranks) {
     __shared__ uint32_t has[kMapEach / 4];
+    __shared__ int parts[kWaves][kRankEach];
     if ((int)blockIdx.x >= ranks) {
         const int v0 = ((int)blockIdx.x - ranks) * kMapEach;
         has[threadIdx.x] = 0;
         __syncthreads();
-        constexpr int B = 4;
+        constexpr int B = 8;
         for (int i = threadIdx.x; i < tokens; i += B * kThreads) {
             uint32_t k[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) k[b] = i + b * kThreads < tokens ? key_of(ids[i + b * kThreads], vocab) - (uint32_t)v0 : ~0u;
+            for (int b = 0; b < B; ++b) {          // past the end: the last token once more
+                const int j = i + b * kThreads;
+                k[b] = key_of(ids[j < tokens ? j : tokens - 1], vocab) - (uint32_t)v0;
+            }
 #pragma unroll
             for (int b = 0; b < B; ++b)
                 if (k[b] < kMapEach) ((uint8_t *)has)[k[b]] = 1;
@@ -109,8 +118,7 @@ __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids
         return;
     }
     const int lane = threadIdx.x & 63;
-    const int t0 = uniform((blockIdx.x * kWaves + (threadIdx.x >> 6)) * kRankEach);
-    if (t0 >= tokens) return;
+    const int wave = uniform(threadIdx.x >> 6), t0 = blockIdx.x * kRankEach;
     uint32_t mine[kRankEach];
     int before[kRankEach];
 #pragma unroll
@@ -118,27 +126,43 @@ __global__ __launch_bounds__(kThreads) void embed_rank_kernel(const int64_t *ids
         mine[k] = t0 + k < tokens ? key_of(ids[t0 + k], vocab) : 0u;
         before[k] = 0;
     }
-    constexpr int B = 4;
-    for (int j0 = 0; j0 < tokens; j0 += 64 * B) {
+    // Tokens in front of this wave's count where their keys are not above, those behind where they are below.
+    const auto count = [&](uint32_t other, uint32_t equal) {
+#pragma unroll
+        for (int k = 0; k < kRankEach; ++k) before[k] += other < mine[k] + equal ? 1 : 0;
+    };
+    // Past the end: after everything.  (Read in bounds rather than skipped, so that no load waits for the one before.)
+    const auto key_at = [&](int j) {
+        const uint32_t key = key_of(ids[j < tokens ? j : tokens - 1], vocab);
+        return j < tokens ? key : ~0u;
+    };
+    constexpr int B = 4, kStep = 64 * kWaves;      // steps whose loads are in flight
+    const int own = t0 / 64 * 64;      // the step that holds these tokens
+    for (int j0 = wave * 64; j0 < tokens; j0 += kStep * B) {
         uint32_t other[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const int j = j0 + b * 64 + lane;
-            other[b] = j < tokens ? key_of(ids[j], vocab) : ~0u;      // past the end: after everything
-        }
+        for (int b = 0; b < B; ++b) other[b] = key_at(j0 + b * kStep + lane);
 #pragma unroll
         for (int b = 0; b < B; ++b)
+            if (j0 + b * kStep != own) count(other[b], j0 + b * kStep < own ? 1 : 0);
+    }
+    if (wave == 0) {
+        const uint32_t other = key_at(own + lane);
 #pragma unroll
-            for (int k = 0; k < kRankEach; ++k)
-                before[k] += (other[b] < mine[k] || (other[b] == mine[k] && j0 + b * 64 + lane < t0 + k)) ? 1 : 0;
+        for (int k = 0; k < kRankEach; ++k) before[k] += other < mine[k] + (own + lane < t0 + k ? 1 : 0) ? 1 : 0;
     }
 #pragma unroll
     for (int k = 0; k < kRankEach; ++k) {
         each_bit([&](auto m) { before[k] += (int)lane_xor<m.value>((uint32_t)before[k], lane); });
-        if (t0 + k < tokens && lane == 0) {
-            keys[before[k]] = mine[k];
-            order[before[k]] = (uint32_t)(t0 + k);
-        }
+        if (lane == 0) parts[wave][k] = before[k];
+    }
+    __syncthreads();
+    const int k = threadIdx.x;
+    if (k < kRankEach && t0 + k < tokens) {
+        int place = 0;
+        for (int w = 0; w < kWaves; ++w) place += parts[w][k];
+        keys[place] = key_of(ids[t0 + k], vocab);
+        order[place] = (uint32_t)(t0 + k);
     }
 }
 
@@ -474,6 +498,9 @@ template <typename F> hipError_t dispatch_embed(const EmbedCall &c, F &&f) {
     });
 }
 
+// LDS that a workgroup of the sums reserves, so that five share a compute unit: 65536 tokens x 4096 bf16 into 131072
+// entries 313 us with none, 312, 322, 300, 300, 393 with 16, 24, 32, 40, 60 KB; 1021 tokens into 32000 fp32 101, 102, 97, 95, 93, 91.
+constexpr size_t kSumLds = 32 * 1024;
 constexpr long long kMostGroups = 1 << 22;             // a grid's threads stay below 2^32
 // Slices of 64 runs of a row.
 int slices_of(const EmbedCall &c) {
@@ -509,7 +536,7 @@ EmbedSpace embed_space(long long tokens, int width, int vocab) {
     w.keys = add(tokens * 4);
     w.order = add(tokens * 4);
     w.map = add((size_t)(vocab + kMapEach - 1) / kMapEach * kMapEach);
-    if (tokens > 8192) {
+    if (tokens > kRankTokens) {
         int bits = 1;
         while ((1 << bits) <= vocab) ++bits;            // the key `vocab` among them
         w.passes = bits <= 11 ? 1 : 2;
@@ -529,7 +556,7 @@ EmbedSpace embed_space(long long tokens, int width, int vocab) {
 hipError_t launch_embed_sort(const EmbedCall &c, const EmbedSpace &w, char *space, hipStream_t s) {
     uint32_t *keys = (uint32_t *)(space + w.keys), *order = (uint32_t *)(space + w.order);
     if (w.passes == 0) {
-        const int ranks = (int)((c.tokens + kWaves * kRankEach - 1) / (kWaves * kRankEach));
+        const int ranks = (int)((c.tokens + kRankEach - 1) / kRankEach);
         const int maps = c.accumulate ? 0 : (c.vocab + kMapEach - 1) / kMapEach;
         return launch(embed_rank_kernel, dim3((unsigned)(ranks + maps)), dim3(kThreads), 0, s, c.ids, (int)c.tokens, c.vocab, keys, order,
                       (uint8_t *)(space + w.map), ranks);
@@ -579,7 +606,7 @@ hipError_t launch_embed_sum(const EmbedCall &c, const EmbedSpace &w, char *space
         hipError_t st = hipSuccess;
         if (a.sums + zeros)
             st = launch(embed_sum_kernel<dt.value, ot.value, tiny.value, nr.value>, dim3((unsigned)(a.sums + zeros)),
-                        dim3(kThreads), 0, s, e, a);
+                        dim3(kThreads), kSumLds, s, e, a);
         if (st == hipSuccess && w.pieces > 1)
             st = launch(embed_join_kernel<dt.value, kCols<dt.value, ot.value>, nr.value>, dim3((unsigned)((w.pieces - 1) * a.slices)), dim3(kThreads), 0, s,
                         e, a);

@@ -155,7 +155,7 @@ def test_gradient(width, dtype, out_dtype):
 
 
 @pytest.mark.parametrize("kind", ["one", "none", "text", "any"])
-@pytest.mark.parametrize("count", [1, 15, 16, 17, 63, 64, 65, 1000, 8191, 8192, 8193, 20000, 70001])
+@pytest.mark.parametrize("count", [1, 15, 16, 17, 63, 64, 65, 1000, 8191, 8192, 8193, 10240, 10241, 20000, 70001])
 def test_gradient_counts(kind, count):
     gradient(tokens_of(kind, count, 3001, seed=count), split(3001, 8), 40, "f32", "bf16")
 
