@@ -628,8 +628,22 @@ for _f in (_lib.ar_reduce_norm, _lib.ar_norm_workspace, _lib.ar_reduce_norm_back
            _lib.ar_clip_grads):
     _f.restype = ctypes.c_int
 
-_TYPES = {DTYPES["f32"]: "torch.float32", DTYPES["bf16"]: "torch.bfloat16", DTYPES["f16"]: "torch.float16"}
-_BYTES = ("torch.float8_e4m3fn", "torch.uint8")
+try:
+    # torch types of a tensor argument by the shape's type code; none where the call itself refuses the code
+    _TYPES = {DTYPES["f32"]: (torch.float32,), DTYPES["bf16"]: (torch.bfloat16,), DTYPES["f16"]: (torch.float16,)}
+    _F32, _I64, _BYTES = (torch.float32,), (torch.int64,), (torch.float8_e4m3fn, torch.uint8)
+except NameError:
+    _TYPES, _F32, _I64, _BYTES = {}, (), (), ()
+
+_device_state = []  # [current-device getter] once known
+
+
+def _device():
+    """torch's current device; -2, which no tensor is on, without torch or a GPU."""
+    if not _device_state:
+        gpu = bool(_TYPES) and torch.cuda.is_available()
+        _device_state.append(torch._C._cuda_getDevice if gpu else lambda: -2)
+    return _device_state[0]()
 
 
 def _longs(values, n, what):
@@ -653,6 +667,8 @@ class NormShape:
         self.pitches = [self.width] * self.n if pitches is None else [int(p) for p in pitches]
         self._pitches = _longs(self.pitches, self.n, "pitch")
         self.groups = -(-self.width // self.group) if self.group > 0 else 1
+        self._types, self._weight_types = _TYPES.get(self.dtype, ()), _TYPES.get(self.weight_dtype, ())
+        self._key = (self, "partials")
         self._struct = _NormStruct(self.n, self.dtype, self.weight_dtype, self.rows, self.width, self._pitches, self.eps,
                                    self.offset, self.group)
         self.ref = ctypes.byref(self._struct)
@@ -673,6 +689,7 @@ class EmbedShape:
         self.pitches = [self.width] * self.n if pitches is None else [int(p) for p in pitches]
         self.grad_pitches = self.pitches if grad_pitches is None else [int(p) for p in grad_pitches]
         self.scale = float(scale)
+        self._out_types, self._table_key, self._grads_key = _TYPES.get(self.out_dtype, ()), (self, "tables"), (self, "grads")
         self._arrays = (_longs(self.entries, self.n, "entry"), _longs(self.pitches, self.n, "pitch"),
                         _longs(self.grad_pitches, self.n, "pitch"))
         self._struct = _EmbedStruct(self.n, self.dtype, self.out_dtype, self.tokens, self.width, *self._arrays, self.scale)
@@ -697,12 +714,13 @@ class GradList:
 
     def __init__(self, tensors):
         self._tensors = list(tensors)
-        self.host, self.count, self._layouts = [], len(self._tensors), []
+        self.host, self.count, self._layouts, self._alike = [], len(self._tensors), [], self
+        device = _device()
         for t in self._tensors:
             if not _dense(t):
                 raise ValueError("gradients must fill their memory; got strides %s" % (tuple(t.stride()),))
             self._layouts.append((t.dtype, tuple(t.shape), tuple(t.stride())))
-            _reachable(t, "gradients", self.host)
+            _reachable(t, "gradients", self.host, device)
         m = max(1, self.count)
         self.sizes = [t.numel() for t in self._tensors]
         self._bufs = (ctypes.c_void_p * m)(*[t.data_ptr() or None for t in self._tensors])
@@ -713,63 +731,71 @@ class GradList:
 
     def like(self, other):
         """Whether ``other`` has the same types, shapes and strides, buffer by buffer."""
-        return other is self or self._layouts == other._layouts
+        if self._alike is not other:
+            if self._layouts != other._layouts:
+                return False
+            self._alike = other            # the last one found alike; lists do not change
+        return True
 
 
-def _reachable(t, what, host):
+def _reachable(t, what, host, device):
     """Notes a tensor in host memory by name (as ``_on_host``) and refuses one on another device than the current one."""
-    if t.is_cuda:
-        if t.get_device() != torch.cuda.current_device():
-            raise ValueError("%s must be on the current device, not on device %d" % (what, t.get_device()))
-    elif _on_host(t):
-        host.append(what)
+    d = t.get_device()
+    if d != device:
+        if d >= 0:
+            raise ValueError("%s must be on the current device (%d), not on device %d" % (what, device, d))
+        if _on_host(t):
+            host.append(what)
 
 
-def _packed(t, dtypes, numel, what, host):
+def _packed(t, dtypes, numel, what, host, device):
     """Address of a contiguous tensor argument of one of ``dtypes`` (integer addresses and None pass through)."""
     if t is None or isinstance(t, int):
         return t
-    if str(t.dtype) not in dtypes or t.numel() < numel or not t.is_contiguous():
+    if t.dtype not in dtypes or t.numel() < numel or not t.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of %s with at least %d elements"
-                         % (what, " or ".join(dtypes), numel))
-    _reachable(t, what, host)
+                         % (what, " or ".join(str(d) for d in dtypes), numel))
+    if t.get_device() != device:
+        _reachable(t, what, host, device)
     return t.data_ptr() or None
 
 
-def _rank_rows(bufs, key, dtype, rows, width, pitches, what, host):
-    """Pointer table of rank buffers; tensors must have the type and hold ``rows[r]`` rows at ``pitches[r]``."""
+def _rank_rows(bufs, key, dtype, rows, width, pitches, host, device):
+    """Pointer table of rank buffers; tensors must have the type and hold ``rows[r]`` rows (one number: each) at
+    ``pitches[r]``.  A table is looked over once for a shape."""
     if not isinstance(bufs, PointerTable):
         bufs = PointerTable(bufs)
     if bufs._checked != key:
+        rows = [rows] * len(pitches) if isinstance(rows, int) else rows
         if bufs.n != len(rows):
             raise ValueError("%d rank buffers for %d ranks" % (bufs.n, len(rows)))
         at = len(host)
         for b, r, p in zip(bufs._bufs, rows, pitches):
             if b is None or isinstance(b, int) or r == 0:
                 continue
-            _rows_at(b, dtype, r, width, p, what, host)
+            _rows_at(b, dtype, r, width, p, key[1], host, device)
         if len(host) == at:
             bufs._checked = key
     return bufs.array
 
 
-def _rows_at(b, dtype, rows, width, pitch, what, host):
-    if str(b.dtype) != _TYPES.get(dtype):
+def _rows_at(b, dtype, rows, width, pitch, what, host, device):
+    if b.dtype not in _TYPES.get(dtype, ()):
         raise ValueError("%s of %s do not have the shape's dtype" % (what, b.dtype))
     room = b.untyped_storage().nbytes() // b.element_size() - b.storage_offset()
     if room < (rows - 1) * pitch + width:
         raise ValueError("%s: a buffer of %d elements; %d rows of %d at pitch %d need more" % (what, room, rows, width, pitch))
     if not _at_pitch(b, pitch, rows):
         raise ValueError("%s have strides %s; their pitch is %d" % (what, tuple(b.stride()), pitch))
-    _reachable(b, what, host)
+    _reachable(b, what, host, device)
 
 
-def _space(w, host):
+def _space(w, host, device):
     if w is None:
         return None, 0
     if not w.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _reachable(w, "workspace", host)
+    _reachable(w, "workspace", host, device)
     return w.data_ptr() or None, w.numel() * w.element_size()
 
 
@@ -784,14 +810,13 @@ def ar_reduce_norm(partials, shape, weight, out=None, residual=None, summed=None
     (``out``; ``out8`` with ``scales``: e4m3 values, a scale to each row or
     group of columns).  ``rstd`` is what ``ar_reduce_norm_backward`` needs
     beside ``summed``."""
-    host, r, w = [], shape.rows, shape.width
-    dt = (_TYPES.get(shape.dtype),)
-    args = (_rank_rows(partials, (shape, "partials"), shape.dtype, [r] * shape.n, w, shape.pitches, "partials", host), shape.ref,
-            _packed(weight, (_TYPES.get(shape.weight_dtype),), w, "weight", host),
-            _packed(residual, dt, r * w, "residual", host), _packed(summed, dt, r * w, "summed", host),
-            _packed(out, dt, r * w, "out", host), _packed(rstd, ("torch.float32",), r, "rstd", host),
-            _packed(out8, _BYTES, r * w, "out8", host),
-            _packed(scales, ("torch.float32",), r * shape.groups, "scales", host))
+    host, r, w, dt, dev = [], shape.rows, shape.width, shape._types, _device()
+    size = r * w
+    args = (_rank_rows(partials, shape._key, shape.dtype, r, w, shape.pitches, host, dev), shape.ref,
+            _packed(weight, shape._weight_types, w, "weight", host, dev), _packed(residual, dt, size, "residual", host, dev),
+            _packed(summed, dt, size, "summed", host, dev), _packed(out, dt, size, "out", host, dev),
+            _packed(rstd, _F32, r, "rstd", host, dev), _packed(out8, _BYTES, size, "out8", host, dev),
+            _packed(scales, _F32, r * shape.groups, "scales", host, dev))
     _refuse_host(host, r)
     _check(_lib.ar_reduce_norm(*args, _stream(stream)))
 
@@ -808,19 +833,18 @@ def ar_reduce_norm_backward(x, shape, weight, rstd, grad_out, grad_x, grad_summe
     """Gradient of the residual and of every partial (``grad_x``), and of the
     weight, from that of ``out`` and, optionally, of ``summed``.  ``x`` is
     ``summed`` (its rows may be apart), ``rstd`` from ``ar_reduce_norm``."""
-    host, r, w = [], shape.rows, shape.width
-    dt, f32 = (_TYPES.get(shape.dtype),), ("torch.float32",)
-    pitch = 0
+    host, r, w, dt, dev = [], shape.rows, shape.width, shape._types, _device()
+    pitch, size = 0, r * w
     if x is not None and not isinstance(x, int):
         pitch = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else w
         if r:
-            _rows_at(x, shape.dtype, r, w, pitch, "x", host)
+            _rows_at(x, shape.dtype, r, w, pitch, "x", host, dev)
         x = x.data_ptr() or None
-    ws, wb = _space(workspace, host)
-    args = (x, pitch, shape.ref, _packed(weight, (_TYPES.get(shape.weight_dtype),), w, "weight", host),
-            _packed(rstd, f32, r, "rstd", host), _packed(grad_out, dt, r * w, "grad_out", host),
-            _packed(grad_summed, dt, r * w, "grad_summed", host), _packed(grad_x, dt, r * w, "grad_x", host),
-            _packed(grad_weight, f32, w, "grad_weight", host))
+    ws, wb = _space(workspace, host, dev)
+    args = (x, pitch, shape.ref, _packed(weight, shape._weight_types, w, "weight", host, dev),
+            _packed(rstd, _F32, r, "rstd", host, dev), _packed(grad_out, dt, size, "grad_out", host, dev),
+            _packed(grad_summed, dt, size, "grad_summed", host, dev), _packed(grad_x, dt, size, "grad_x", host, dev),
+            _packed(grad_weight, _F32, w, "grad_weight", host, dev))
     _refuse_host(host)
     _check(_lib.ar_reduce_norm_backward(*args, ws, wb, _stream(stream)))
 
@@ -828,10 +852,10 @@ def ar_reduce_norm_backward(x, shape, weight, rstd, grad_out, grad_x, grad_summe
 def ar_embedding(tables, shape, token_ids, out, stream=None):
     """The tokens' rows of a table split by vocabulary entries over the n rank
     buffers, times the scale; zeros for a token outside the vocabulary."""
-    host, t = [], shape.tokens
-    args = (_rank_rows(tables, (shape, "tables"), shape.dtype, shape.entries, shape.width, shape.pitches, "tables", host),
-            shape.ref, _packed(token_ids, ("torch.int64",), t, "token_ids", host),
-            _packed(out, (_TYPES.get(shape.out_dtype),), t * shape.width, "out", host))
+    host, t, dev = [], shape.tokens, _device()
+    args = (_rank_rows(tables, shape._table_key, shape.dtype, shape.entries, shape.width, shape.pitches, host, dev), shape.ref,
+            _packed(token_ids, _I64, t, "token_ids", host, dev),
+            _packed(out, shape._out_types, t * shape.width, "out", host, dev))
     _refuse_host(host, t)
     _check(_lib.ar_embedding(*args, _stream(stream)))
 
@@ -846,11 +870,11 @@ def ar_embedding_workspace(shape) -> int:
 def ar_embedding_backward(grad_out, shape, token_ids, grads, accumulate=False, workspace=None, stream=None):
     """Gradient of every rank's part of the table, zeros in the rows of entries
     without a token; or, with ``accumulate``, added to what the buffers hold."""
-    host, t = [], shape.tokens
-    ws, wb = _space(workspace, host)
-    table = _rank_rows(grads, (shape, "grads"), shape.dtype, shape.entries, shape.width, shape.grad_pitches, "grads", host)
-    args = (_packed(grad_out, (_TYPES.get(shape.out_dtype),), t * shape.width, "grad_out", host), shape.ref,
-            _packed(token_ids, ("torch.int64",), t, "token_ids", host), table, int(bool(accumulate)))
+    host, t, dev = [], shape.tokens, _device()
+    ws, wb = _space(workspace, host, dev)
+    table = _rank_rows(grads, shape._grads_key, shape.dtype, shape.entries, shape.width, shape.grad_pitches, host, dev)
+    args = (_packed(grad_out, shape._out_types, t * shape.width, "grad_out", host, dev), shape.ref,
+            _packed(token_ids, _I64, t, "token_ids", host, dev), table, int(bool(accumulate)))
     _refuse_host(host, t or not accumulate)
     _check(_lib.ar_embedding_backward(*args, ws, wb, _stream(stream)))
 
@@ -864,9 +888,9 @@ def ar_grad_workspace(grads) -> int:
 
 def ar_grad_norm(grads, norm, scale=1.0, workspace=None, stream=None):
     """``scale`` times the 2-norm of all buffers of a ``GradList`` taken together."""
-    host = list(grads.host)
-    ws, wb = _space(workspace, host)
-    norm = _packed(norm, ("torch.float32",), 1, "norm", host)
+    host, dev = list(grads.host), _device()
+    ws, wb = _space(workspace, host, dev)
+    norm = _packed(norm, _F32, 1, "norm", host, dev)
     _refuse_host(host)
     _check(_lib.ar_grad_norm(grads.ref, scale, norm, ws, wb, _stream(stream)))
 
@@ -877,8 +901,8 @@ def ar_clip_grads(grads, outs, norm, max_norm, scale=1.0, eps=1e-6, workspace=No
     when ``outs`` is ``grads``)."""
     if not grads.like(outs):
         raise ValueError("outs must have the types, shapes and strides of grads")
-    host = grads.host + outs.host
-    ws, wb = _space(workspace, host)
-    norm = _packed(norm, ("torch.float32",), 1, "norm", host)
+    host, dev = grads.host + outs.host, _device()
+    ws, wb = _space(workspace, host, dev)
+    norm = _packed(norm, _F32, 1, "norm", host, dev)
     _refuse_host(host)
     _check(_lib.ar_clip_grads(grads.ref, outs._bufs, max_norm, scale, eps, norm, ws, wb, _stream(stream)))
