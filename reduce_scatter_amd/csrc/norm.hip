@@ -473,7 +473,11 @@ hipError_t launch_reduce_norm(const NormCall &c, hipStream_t s) {
 NormBackPlan norm_back_plan(int dtype, long long rows, int width) {
     const RowPlan p = plan_row(dtype, width);
     const long long sets = p.lanes ? kShortThreads / p.lanes : 1;
-    const long long groups = (rows + sets - 1) / sets, most = 256LL * (p.lanes ? 8 : 1024 / p.threads);
+    // Workgroups to a compute unit, up to 16 waves of them; each leaves a partial weight gradient that is written and
+    // read once more.  us with 1, 2, 3, 4, 8 to a unit: 777 x 5003 fp32 (10 waves) 19, 21, 24, 25, 25; 2048 x 4096
+    // bf16 (8) 15.2, 16.9, 19.0, 22.5, 27.8; 16384 x 2048 (4) 55, 42, 39, 42, 49; 8192 x 1024 (2) 27, 20, 18, 18, 21;
+    // 65536 x 256 (a wave to a row, 4 rows) 55, 36, 33, 32, 36.
+    const long long groups = (rows + sets - 1) / sets, most = 256LL * (1024 / p.threads < 4 ? 1024 / p.threads : 4);
     return {(int)(groups < most ? groups : most), p.lanes ? width : p.u * (dtype == F32 ? 4 : 8) * p.threads};
 }
 
