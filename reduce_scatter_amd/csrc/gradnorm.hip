@@ -60,6 +60,7 @@ template <int DT, bool STREAM> __device__ __forceinline__ void add_squares(const
     }
 }
 
+// 2.75 GB: 399 us, 6.9 TB/s; 69 MB: 14 us (16 with half as many workgroups).
 template <bool STREAM> __global__ __launch_bounds__(kThreads, 8) void grad_sum_kernel(const GradTable t) {
     __shared__ double lds[kWaves];
     const int lane = threadIdx.x & 63;
@@ -119,6 +120,8 @@ template <int DT> __device__ __forceinline__ void scale_chunk(const char *in, ch
 }
 
 // A workgroup scales one chunk: 8 KB each, in the order of their addresses.
+// 2.75 GB in bf16 and fp32: 870 us, 6.3 TB/s; dealt out to 1024 or 2048 workgroups
+// that stay, 967 and 1040.
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable t) {
     __shared__ double lds[kWaves];
     const double norm = t.parts ? whole_norm<kWaves>(t, lds) : *t.wide;

