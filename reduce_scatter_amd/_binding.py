@@ -634,6 +634,7 @@ try:
     _F32, _I64, _BYTES = (torch.float32,), (torch.int64,), (torch.float8_e4m3fn, torch.uint8)
 except NameError:
     _TYPES, _F32, _I64, _BYTES = {}, (), (), ()
+_CODES = {types[0]: code for code, types in _TYPES.items()}
 
 _device_state = []  # [current-device getter] once known
 
@@ -715,17 +716,20 @@ class GradList:
     def __init__(self, tensors):
         self._tensors = list(tensors)
         self.host, self.count, self._layouts, self._alike = [], len(self._tensors), [], self
-        device = _device()
+        device, codes = _device(), []
         for t in self._tensors:
-            if not _dense(t):
+            if not t.is_contiguous() and not _dense(t):
                 raise ValueError("gradients must fill their memory; got strides %s" % (tuple(t.stride()),))
-            self._layouts.append((t.dtype, tuple(t.shape), tuple(t.stride())))
-            _reachable(t, "gradients", self.host, device)
+            self._layouts.append((t.dtype, t.shape, t.stride()))
+            if t.get_device() != device:
+                _reachable(t, "gradients", self.host, device)
+            code = _CODES.get(t.dtype)
+            codes.append(_dtype_code(t.dtype) if code is None else code)
         m = max(1, self.count)
         self.sizes = [t.numel() for t in self._tensors]
         self._bufs = (ctypes.c_void_p * m)(*[t.data_ptr() or None for t in self._tensors])
         self._sizes = (ctypes.c_longlong * m)(*self.sizes)
-        self._dtypes = (ctypes.c_int * m)(*[_dtype_code(t.dtype) for t in self._tensors])
+        self._dtypes = (ctypes.c_int * m)(*codes)
         self._struct = _GradsStruct(self.count, ctypes.cast(self._bufs, ctypes.c_void_p), self._sizes, self._dtypes)
         self.ref = ctypes.byref(self._struct)
 
