@@ -12,8 +12,9 @@
  *   rstd  = 1 / sqrt(mean(s^2) + eps)
  *   y_c   = s_c * rstd * (offset + weight_c)
  *   out, summed   y and s rounded to the storage type (y from the unrounded s)
- *   out8, scales  e4m3 (OCP: largest value 448) of y / scale, rounded to nearest
- *                 even, with scale = max |y| / 448, but 2^-100 at least, over
+ *   out8, scales  e4m3 (OCP: largest value 448) of y / scale, y and the quotient
+ *                 being fp32 numbers, rounded to nearest even, with
+ *                 scale = max |y| / 448, but 2^-100 at least, over
  *                 the row (group 0) or over every `group` columns (the last
  *                 group may be short); where some |y| is not finite, scale and
  *                 the group's values are NaN
@@ -36,10 +37,10 @@
  * f = max_norm / (norm + eps) where that is below 1, else 1; NaN everywhere
  * where norm is NaN, and f = 0 where it is infinite.
  *
- * Arithmetic: fp32 and 64 bits as stated; results are rounded once, to nearest
- * even, to the type they are stored in.  Sums are taken in an order fixed by
- * the shape (for the gradient norm: by the list and by which of its buffers
- * adjoin), so equal calls give equal bits.
+ * Arithmetic: fp32 (rstd's root to within a step) and 64 bits as stated; results
+ * are rounded once, to nearest even, to the type they are stored in.  Sums are
+ * taken in an order fixed by the shape (for the gradient norm: by the list and by
+ * which of its buffers adjoin), so equal calls give equal bits.
  *
  * Buffers: arrays of pointers are HOST arrays of DEVICE pointers, read during
  * the call only.  Everything else is a device pointer to contiguous row-major
