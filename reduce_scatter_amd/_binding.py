@@ -841,6 +841,8 @@ def ar_reduce_norm_backward(x, shape, weight, rstd, grad_out, grad_x, grad_summe
     pitch, size = 0, r * w
     if x is not None and not isinstance(x, int):
         pitch = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else w
+        if r > 1 and pitch < w:            # 0 would mean the width to the library
+            raise ValueError("x has rows at a pitch of %d elements; they hold %d" % (pitch, w))
         if r:
             _rows_at(x, shape.dtype, r, w, pitch, "x", host, dev)
         x = x.data_ptr() or None

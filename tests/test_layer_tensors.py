@@ -1,0 +1,62 @@
+"""What the binding hands to the library's layer operators for tensors of unusual
+layouts, without a GPU: the library is replaced by a record of its calls, and
+host tensors say that they are on a device."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+ar = pytest.importorskip("reduce_scatter_amd", reason="libar.so not built")
+
+from reduce_scatter_amd import _binding as b  # noqa: E402
+
+ADDR = 1 << 24
+
+
+class OnDevice(torch.Tensor):
+    index = 0
+
+    def get_device(self):
+        return type(self).index
+
+
+class Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(b, "_lib", r)
+    monkeypatch.setattr(b, "_device", lambda: 0)
+    monkeypatch.setattr(OnDevice, "index", 0)
+    return r.calls
+
+
+def tensor(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def backward(x, rows, width):
+    ar.ar_reduce_norm_backward(x, ar.NormShape(rows, width, 1, "f32"), ADDR, ADDR * 2, ADDR * 3, ADDR * 4, stream=0)
+
+
+@pytest.mark.parametrize("x", [tensor(1, 64).expand(4, 64), tensor(1, 1, 64).expand(2, 2, 64),
+                               tensor(64).as_strided((4, 64), (0, 1)), tensor(256).as_strided((4, 64), (63, 1))])
+def test_rows_that_share_memory_are_refused(calls, x):
+    """A pitch of 0 means the width to the library, which would read past a row that all rows share."""
+    with pytest.raises(ValueError, match="pitch"):
+        backward(x, 4, 64)
+    assert not calls
+
+
+def test_rows_apart_and_one_row(calls):
+    backward(tensor(4, 70)[:, :64], 4, 64)
+    backward(tensor(4, 64), 4, 64)
+    backward(tensor(64), 1, 64)
+    backward(tensor(1, 64).expand(1, 64), 1, 64)
+    assert [args[1] for _, args in calls] == [70, 64, 64, 64]
