@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import weakref
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -715,7 +716,7 @@ class GradList:
 
     def __init__(self, tensors):
         self._tensors = list(tensors)
-        self.host, self.count, self._layouts, self._alike = [], len(self._tensors), [], self
+        self.host, self.count, self._layouts, self._alike = [], len(self._tensors), [], None
         device, codes = _device(), []
         for t in self._tensors:
             if not t.is_contiguous() and not _dense(t):
@@ -735,10 +736,11 @@ class GradList:
 
     def like(self, other):
         """Whether ``other`` has the same types, shapes and strides, buffer by buffer."""
-        if self._alike is not other:
-            if self._layouts != other._layouts:
-                return False
-            self._alike = other            # the last one found alike; lists do not change
+        if other is self or (self._alike is not None and self._alike() is other):
+            return True
+        if self._layouts != other._layouts:
+            return False
+        self._alike = weakref.ref(other)   # the last one found alike, not kept alive; lists do not change
         return True
 
 
