@@ -670,7 +670,7 @@ class NormShape:
         self._pitches = _longs(self.pitches, self.n, "pitch")
         self.groups = -(-self.width // self.group) if self.group > 0 else 1
         self._types, self._weight_types = _TYPES.get(self.dtype, ()), _TYPES.get(self.weight_dtype, ())
-        self._key = (self, "partials")
+        self._key = (object(), "partials")     # one of its own, by which a table knows the shape it was looked over for
         self._struct = _NormStruct(self.n, self.dtype, self.weight_dtype, self.rows, self.width, self._pitches, self.eps,
                                    self.offset, self.group)
         self.ref = ctypes.byref(self._struct)
@@ -691,7 +691,7 @@ class EmbedShape:
         self.pitches = [self.width] * self.n if pitches is None else [int(p) for p in pitches]
         self.grad_pitches = self.pitches if grad_pitches is None else [int(p) for p in grad_pitches]
         self.scale = float(scale)
-        self._out_types, self._table_key, self._grads_key = _TYPES.get(self.out_dtype, ()), (self, "tables"), (self, "grads")
+        self._out_types, self._table_key, self._grads_key = _TYPES.get(self.out_dtype, ()), (object(), "tables"), (object(), "grads")
         self._arrays = (_longs(self.entries, self.n, "entry"), _longs(self.pitches, self.n, "pitch"),
                         _longs(self.grad_pitches, self.n, "pitch"))
         self._struct = _EmbedStruct(self.n, self.dtype, self.out_dtype, self.tokens, self.width, *self._arrays, self.scale)

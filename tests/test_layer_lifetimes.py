@@ -49,3 +49,11 @@ def test_a_list_compared_with_itself_and_others():
     assert lst.like(other)
     del lst
     assert freed()
+
+
+def test_shapes_go_with_their_last_reference():
+    for build in (lambda: ar.NormShape(4, 16, 2, "f32"), lambda: ar.EmbedShape(4, [8, 8], 16, "f32")):
+        shape = build()
+        ref = weakref.ref(shape)
+        del shape
+        assert ref() is None
