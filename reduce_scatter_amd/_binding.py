@@ -717,13 +717,13 @@ class GradList:
     def __init__(self, tensors):
         self._tensors = list(tensors)
         self.host, self.count, self._layouts, self._alike = [], len(self._tensors), [], None
-        device, codes = _device(), []
+        self._device, codes = _device(), []
         for t in self._tensors:
             if not t.is_contiguous() and not _dense(t):
                 raise ValueError("gradients must fill their memory; got strides %s" % (tuple(t.stride()),))
             self._layouts.append((t.dtype, t.shape, t.stride()))
-            if t.get_device() != device:
-                _reachable(t, "gradients", self.host, device)
+            if t.get_device() != self._device:
+                _reachable(t, "gradients", self.host, self._device)
             code = _CODES.get(t.dtype)
             codes.append(_dtype_code(t.dtype) if code is None else code)
         m = max(1, self.count)
@@ -733,6 +733,15 @@ class GradList:
         self._dtypes = (ctypes.c_int * m)(*codes)
         self._struct = _GradsStruct(self.count, ctypes.cast(self._bufs, ctypes.c_void_p), self._sizes, self._dtypes)
         self.ref = ctypes.byref(self._struct)
+
+    def on_host(self, device):
+        """Names of what no kernel of ``device``, the current one, reaches; refuses tensors on another one."""
+        if device != self._device:
+            host = []
+            for t in self._tensors:
+                _reachable(t, "gradients", host, device)
+            self.host, self._device = host, device
+        return self.host
 
     def like(self, other):
         """Whether ``other`` has the same types, shapes and strides, buffer by buffer."""
@@ -768,10 +777,10 @@ def _packed(t, dtypes, numel, what, host, device):
 
 def _rank_rows(bufs, key, dtype, rows, width, pitches, host, device):
     """Pointer table of rank buffers; tensors must have the type and hold ``rows[r]`` rows (one number: each) at
-    ``pitches[r]``.  A table is looked over once for a shape."""
+    ``pitches[r]``.  A table is looked over once for a shape and device."""
     if not isinstance(bufs, PointerTable):
         bufs = PointerTable(bufs)
-    if bufs._checked != key:
+    if bufs._checked != (key, device):
         rows = [rows] * len(pitches) if isinstance(rows, int) else rows
         if bufs.n != len(rows):
             raise ValueError("%d rank buffers for %d ranks" % (bufs.n, len(rows)))
@@ -781,7 +790,7 @@ def _rank_rows(bufs, key, dtype, rows, width, pitches, host, device):
                 continue
             _rows_at(b, dtype, r, width, p, key[1], host, device)
         if len(host) == at:
-            bufs._checked = key
+            bufs._checked = (key, device)
     return bufs.array
 
 
@@ -896,7 +905,8 @@ def ar_grad_workspace(grads) -> int:
 
 def ar_grad_norm(grads, norm, scale=1.0, workspace=None, stream=None):
     """``scale`` times the 2-norm of all buffers of a ``GradList`` taken together."""
-    host, dev = list(grads.host), _device()
+    dev = _device()
+    host = list(grads.on_host(dev))
     ws, wb = _space(workspace, host, dev)
     norm = _packed(norm, _F32, 1, "norm", host, dev)
     _refuse_host(host)
@@ -909,7 +919,8 @@ def ar_clip_grads(grads, outs, norm, max_norm, scale=1.0, eps=1e-6, workspace=No
     when ``outs`` is ``grads``)."""
     if not grads.like(outs):
         raise ValueError("outs must have the types, shapes and strides of grads")
-    host, dev = grads.host + outs.host, _device()
+    dev = _device()
+    host = grads.on_host(dev) + outs.on_host(dev)
     ws, wb = _space(workspace, host, dev)
     norm = _packed(norm, _F32, 1, "norm", host, dev)
     _refuse_host(host)

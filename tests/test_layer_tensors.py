@@ -60,3 +60,27 @@ def test_rows_apart_and_one_row(calls):
     backward(tensor(64), 1, 64)
     backward(tensor(1, 64).expand(1, 64), 1, 64)
     assert [args[1] for _, args in calls] == [70, 64, 64, 64]
+
+
+def test_what_was_looked_over_on_another_device_is_looked_over_again(calls, monkeypatch):
+    """A list or table that fits the current device does not fit another one that becomes current."""
+    grads = ar.GradList([tensor(4), tensor(5)])
+    table, em = ar.pointers([tensor(8, 16), tensor(8, 16)]), ar.EmbedShape(4, [8, 8], 16, "f32")
+    partials, nm = ar.pointers([tensor(4, 16)]), ar.NormShape(4, 16, 1, "f32")
+    todo = [lambda: ar.ar_grad_norm(grads, ADDR, stream=0), lambda: ar.ar_clip_grads(grads, grads, ADDR, 1.0, stream=0),
+            lambda: ar.ar_embedding(table, em, ADDR, ADDR * 2, stream=0),
+            lambda: ar.ar_embedding_backward(ADDR, em, ADDR * 2, table, stream=0),
+            lambda: ar.ar_reduce_norm(partials, nm, ADDR, out=ADDR * 2, stream=0)]
+    for f in todo + todo:
+        f()
+    done = len(calls)
+    assert done == 2 * len(todo)
+    monkeypatch.setattr(b, "_device", lambda: 1)
+    for f in todo:
+        with pytest.raises(ValueError, match="current device"):
+            f()
+    assert len(calls) == done
+    monkeypatch.setattr(b, "_device", lambda: 0)
+    for f in todo:
+        f()
+    assert len(calls) == done + len(todo)
