@@ -805,6 +805,16 @@ def _rows_at(b, dtype, rows, width, pitch, what, host, device):
     _reachable(b, what, host, device)
 
 
+def _pitch_of(x, width):
+    """Elements between a tensor's rows (all its dimensions but the last): the innermost stride of those that hold more
+    than one; the width where no such dimension is left or a row is divided into several (``_rows_at`` has it packed then)."""
+    if x.dim() > 1 and x.shape[-1] >= width:
+        for size, stride in zip(x.shape[-2::-1], x.stride()[-2::-1]):
+            if size > 1:
+                return stride
+    return width
+
+
 def _space(w, host, device):
     if w is None:
         return None, 0
@@ -851,7 +861,7 @@ def ar_reduce_norm_backward(x, shape, weight, rstd, grad_out, grad_x, grad_summe
     host, r, w, dt, dev = [], shape.rows, shape.width, shape._types, _device()
     pitch, size = 0, r * w
     if x is not None and not isinstance(x, int):
-        pitch = x.stride(-2) if x.dim() > 1 and x.shape[-2] > 1 else w
+        pitch = _pitch_of(x, w)
         if r > 1 and pitch < w:            # 0 would mean the width to the library
             raise ValueError("x has rows at a pitch of %d elements; they hold %d" % (pitch, w))
         if r:

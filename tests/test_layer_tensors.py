@@ -84,3 +84,25 @@ def test_what_was_looked_over_on_another_device_is_looked_over_again(calls, monk
     for f in todo:
         f()
     assert len(calls) == done + len(todo)
+
+
+def test_rows_of_one_position_and_of_divided_columns(calls):
+    """The rows of x as [batch, 1, width], cut from a longer buffer or not, and packed rows whose columns are divided."""
+    whole = tensor(4, 7, 64)
+    backward(whole[:, 6:], 4, 64)                      # the last position of each sequence
+    backward(whole[:, 6:, :48], 4, 48)
+    backward(tensor(4, 1, 64), 4, 64)
+    backward(tensor(4, 1, 1, 64), 4, 64)
+    backward(tensor(2, 1, 2, 64), 4, 64)
+    backward(whole[:1, :1], 1, 64)
+    backward(tensor(4, 8, 8), 4, 64)
+    backward(tensor(4, 1, 70)[..., :64], 4, 64)
+    assert [args[1] for _, args in calls] == [448, 448, 64, 64, 64, 64, 64, 70]
+    del calls[:]
+    # rows that are not at one pitch; divided rows that are not packed
+    for x, rows, width in ((whole[:, 5:], 8, 64), (tensor(4, 10, 8)[:, :8], 4, 64), (tensor(2, 4, 64).transpose(0, 1), 8, 64)):
+        with pytest.raises(ValueError, match="strides|need more"):
+            backward(x, rows, width)
+    assert not calls
+    backward(whole[:, :, :48], 28, 48)                 # but these are
+    assert calls[0][1][1] == 64
