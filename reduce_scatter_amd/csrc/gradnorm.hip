@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * kFinishWaves) void grad_finish_kernel(const Gr
 }
 
 // One step of a workgroup: two vectors to a thread.
-template <int DT> __device__ __forceinline__ void scale_chunk(const char *in, char *out, int n, float f) {
+template <int DT> __device__ __forceinline__ void scale_chunk(const char *in, char *out, int n, float f, float again) {
     constexpr int K = Lanes<DT>::value, U = kGradScaleBytes / 16 / kThreads;
     Run<DT, K> o[U];
 #pragma unroll
@@ -115,6 +115,10 @@ template <int DT> __device__ __forceinline__ void scale_chunk(const char *in, ch
         widen<DT, K>(o[u], v);
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] *= f;
+        if (again != 1.0f) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] *= again;
+        }
         store_run<DT, K>(out + (long long)i * elem_bytes<DT>(), narrow<DT, K>(v), n - i);
     }
 }
@@ -128,19 +132,23 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable t)
     if (t.norm && blockIdx.x == 0 && threadIdx.x == 0) *t.norm = (float)norm;
     double f = (double)t.max_norm / (norm + (double)t.eps);
     if (!(f < 1.0)) f = norm != norm ? norm : 1.0;
-    const float factor = (float)(f * (double)t.scale);
+    f *= (double)t.scale;
+    // A factor below fp32's normal numbers would lose digits, or all of it: such a one is taken in two steps.  (1.36 G
+    // elements, norm included, take 1269 us with this branch and 1266 without.)
+    const float again = f < 0x1p-126 ? 0x1p-126f : 1.0f;
+    const float factor = (float)(f < 0x1p-126 ? f * 0x1p126 : f);
     const int e = __builtin_amdgcn_readfirstlane(entry_of(t, blockIdx.x, threadIdx.x & 63));
     // nothing changes in place
-    if (factor == 1.0f && t.in[e] == t.out[e]) return;
+    if (factor == 1.0f && again == 1.0f && t.in[e] == t.out[e]) return;
     const int es = t.dtype[e] == F32 ? 4 : 2, chunk = kGradScaleBytes / es;
     const uint32_t at = (blockIdx.x - t.first[e]) * chunk, left = t.size[e] - at;
     const int n = left < (uint32_t)chunk ? (int)left : chunk;
     const char *in = t.in[e] + (long long)at * es;
     char *out = t.out[e] + (long long)at * es;
     switch (t.dtype[e]) {
-    case F32: scale_chunk<F32>(in, out, n, factor); break;
-    case BF16: scale_chunk<BF16>(in, out, n, factor); break;
-    default: scale_chunk<F16>(in, out, n, factor); break;
+    case F32: scale_chunk<F32>(in, out, n, factor, again); break;
+    case BF16: scale_chunk<BF16>(in, out, n, factor, again); break;
+    default: scale_chunk<F16>(in, out, n, factor, again); break;
     }
 }
 
