@@ -21,7 +21,8 @@
  * Its gradient (ar_reduce_norm_backward): with x the stored s, h = x * rstd, u = grad_out * (offset + weight),
  *   grad_x      = rstd * (u - h * mean(u h)) + grad_summed   (of the residual and of every partial)
  *   grad_weight = sum over the rows of grad_out * h          (fp32; 0 without rows)
- * Squares that leave the range of fp32 are added up in 64 bits.
+ * Squares that leave the range of fp32 are added up in 64 bits; a rstd past it (eps
+ * 0, rows of subnormal numbers) is stored as an infinity, y is finite all the same.
  *
  * Embedding (ar_embedding): out[t] = scale * table[token_t], zeros for a token
  * outside [0, V), V = sum of entries ("no token", e.g. -1).  Rank r holds

@@ -129,9 +129,10 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
         for (int i = 0; i < K; ++i) sq = __builtin_fmaf(s[u][i], s[u][i], sq);
     }
     sq = row_sum<LANES>(sq, lds_sum, waves, wave, lane);
-    float rstd;
+    float rstd, root;                  // what is stored, and what s is multiplied with
+    bool lift = false;                 // rstd may be past fp32, which takes eps = 0 and subnormal numbers: s 2^64, root 2^-64
     if (sq >= 1e-30f && sq <= 1e30f) {
-        rstd = __builtin_amdgcn_rsqf(sq / (float)width + a.r.eps);
+        root = rstd = __builtin_amdgcn_rsqf(sq / (float)width + a.r.eps);
     } else {
         // squares out of fp32's range, or a row of zeros, infinities or NaN
         double wide = 0.0;
@@ -140,7 +141,11 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
 #pragma unroll
             for (int i = 0; i < K; ++i) wide = __builtin_fma((double)s[u][i], (double)s[u][i], wide);
         wide = row_sum<LANES>(wide, lds_wide, waves, wave, lane);
-        rstd = (float)(1.0 / __builtin_sqrt(wide / width + (double)a.r.eps));
+        const double r = 1.0 / __builtin_sqrt(wide / width + (double)a.r.eps);
+        rstd = (float)r;
+        lift = r > 0x1p127 && r < 0x1p300;
+        if (lift) root = (float)(r * 0x1p-64);
+        else root = rstd;
     }
     if (a.rstd && t == 0) a.rstd[row] = rstd;
 
@@ -150,12 +155,18 @@ __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduc
             store_run<DT, K>(a.summed + (packed + p[u].col) * elem_bytes<DT>(), narrow<DT, K>(s[u]), p[u].left);
     }
     if (!a.out && !a.out8) return;
+    if (lift) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < K; ++i) s[u][i] *= 0x1p64f;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float w[K];
         load_weight<DT, K, TINY>(a.r, p[u], w);
 #pragma unroll
-        for (int i = 0; i < K; ++i) s[u][i] = p[u].left > i ? s[u][i] * rstd * w[i] : 0.0f;
+        for (int i = 0; i < K; ++i) s[u][i] = p[u].left > i ? s[u][i] * root * w[i] : 0.0f;
     }
     if (a.out) {
 #pragma unroll
