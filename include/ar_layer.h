@@ -35,8 +35,10 @@
  *
  * Gradient norm: norm = scale * sqrt(sum g^2) over all elements of all buffers,
  * added up in 64 bits.  ar_clip_grads also writes out = g * scale * f,
- * f = max_norm / (norm + eps) where that is below 1, else 1; NaN everywhere
- * where norm is NaN, and f = 0 where it is infinite.
+ * f = max_norm / (norm + eps) where that is below 1, else 1, with the norm in 64
+ * bits (`norm` may be past fp32, an infinity, where it is not).  Where the norm
+ * is NaN, everything is; where a gradient is infinite and max_norm is not, f is
+ * 0; an infinite max_norm never clips (f = 1).
  *
  * Arithmetic: fp32 (rstd's root to within a step) and 64 bits as stated; results
  * are rounded once, to nearest even, to the type they are stored in.  Sums are

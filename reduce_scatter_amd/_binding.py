@@ -926,7 +926,7 @@ def ar_grad_norm(grads, norm, scale=1.0, workspace=None, stream=None):
 def ar_clip_grads(grads, outs, norm, max_norm, scale=1.0, eps=1e-6, workspace=None, stream=None):
     """``ar_grad_norm``, and every buffer times ``scale`` and, where the norm is
     above it, ``max_norm / (norm + eps)``, into the buffers of ``outs`` (in place
-    when ``outs`` is ``grads``)."""
+    when ``outs`` is ``grads``).  An infinite ``max_norm`` never clips."""
     if not grads.like(outs):
         raise ValueError("outs must have the types, shapes and strides of grads")
     dev = _device()
