@@ -82,7 +82,7 @@ __device__ __forceinline__ float quotient(float y, float inv, float rest) { retu
 
 // 16384 x 8192 bf16 from 8 ranks with the residual: 481 us, 6.1 TB/s of 2.95 GB, the
 // same with 4, 8 or 16 waves to a row; 3001 x 5003 fp16 from 4 with both outputs 45
-// us, 5.0 TB/s (rows off 16-byte boundaries); one row of 4096 from 8 ranks 3.1 us.
+// us, 5.0 TB/s (rows off 16-byte boundaries); one row of 4096 from 8 ranks 3.2 us.
 template <int DT, int U, int LANES, bool TINY, int NR>
 __global__ __launch_bounds__(LANES ? kShortThreads : 64 * kNormWaves) void reduce_norm_kernel(const NormArgs<NR> a) {
     __shared__ float lds_sum[kNormWaves];
@@ -509,7 +509,8 @@ NormBackPlan norm_back_plan(int dtype, long long rows, int width) {
     // Workgroups to a compute unit, up to 16 waves of them; each leaves a partial weight gradient that is written and
     // read once more.  us with 1, 2, 3, 4, 8 to a unit: 777 x 5003 fp32 (10 waves) 19, 21, 24, 25, 25; 2048 x 4096
     // bf16 (8) 15.2, 16.9, 19.0, 22.5, 27.8; 16384 x 2048 (4) 55, 42, 39, 42, 49; 8192 x 1024 (2) 27, 20, 18, 18, 21;
-    // 65536 x 256 (a wave to a row, 4 rows) 55, 36, 33, 32, 36.
+    // 65536 x 256 (a wave to a row, 4 rows) 55, 36, 33, 32, 36.  The rule takes the best of three of these; 2048 x 4096
+    // would be 1.7 us faster with one, 16384 x 2048 3 us with three.
     const long long groups = (rows + sets - 1) / sets, most = 256LL * (1024 / p.threads < 4 ? 1024 / p.threads : 4);
     return {(int)(groups < most ? groups : most), p.lanes ? width : p.u * (dtype == F32 ? 4 : 8) * p.threads};
 }
