@@ -36,7 +36,7 @@ def test_factors_below_the_normal_numbers(max_norm, scale, sizes, in_place):
     got = torch.empty(1, device="cuda")
     ar.ar_clip_grads(gl, outs, got, max_norm, scale=scale, eps=0.0,
                      workspace=torch.empty(ar.ar_grad_workspace(gl), dtype=torch.uint8, device="cuda"))
-    assert got.item() == np.float32(norm) or abs(got.item() - norm) <= 1.01 * U * norm
+    assert got.item() == float("inf") if norm > 3.4028236e38 else abs(got.item() - norm) <= 1.01 * U * norm
     for b, o in zip(before, outs._tensors):
         want, (rel, tiny) = b * f, HALF[o.dtype]
         err = np.abs(o.double().cpu().numpy() - want)

@@ -40,7 +40,7 @@ def ids_of(kind, count, vocab):
     return t
 
 
-def check(kind, count, vocab, n, width, dtype, act, pad=0, scale=0.5, calls=1):
+def check(kind, count, vocab, n, width, dtype, act, pad=0, scale=0.5):
     g = torch.Generator(device="cuda").manual_seed(count + width)
     ids = ids_of(kind, count, vocab).astype(np.int64)
     entries = ar.vocab_widths(vocab, n)
